@@ -33,12 +33,25 @@ class QLoRAError(RuntimeError):
 
 QLORA_QUANT_NF4 = 0
 QLORA_QUANT_FP4 = 1
+QLORA_ACT8_INT8 = 0
+QLORA_ACT8_E4M3 = 1
+QLORA_ACT8_BLOCK = 32
+QLORA_LOGITS_BF16 = 0
+QLORA_LOGITS_FP32 = 1
+QLORA_PREF_SIGMOID = 0
+QLORA_PREF_HINGE = 1
+QLORA_PREF_IPO = 2
 
 
 class _Weight(ctypes.Structure):
     _fields_ = [("packed", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
                 ("mean", ctypes.c_void_p), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("quant_type", ctypes.c_int32)]
+
+
+class _Act8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("M", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("fmt", ctypes.c_int32)]
 
 
 def lib():
@@ -69,6 +82,18 @@ def lib():
             "qlora_workspace_bytes": (ctypes.c_size_t, [i64, i64, i64, i32]),
             "qlora_linear_fwd": (i32, [P, i64, WP, P, P, i32, f32, P, P, P, ctypes.c_size_t, P]),
             "qlora_linear_bwd": (i32, [P, P, i64, WP, P, P, i32, f32, P, P, P, P, P, ctypes.c_size_t, P]),
+            "act8_sizes": (i32, [i64, i64, P, P]),
+            "act8_quantize": (i32, [P, i64, i64, i32, P, P, P]),
+            "act8_dequant": (i32, [ctypes.POINTER(_Act8), P, P]),
+            "qlora_act8_workspace_bytes": (ctypes.c_size_t, [i64, i64, i64, i32, i32]),
+            "qlora_linear_bwd_act8": (i32, [ctypes.POINTER(_Act8), P, WP, P, P, i32, f32, f32, u64, u64, P, P, P, P,
+                                            P, ctypes.c_size_t, P]),
+            "loss_workspace_bytes": (ctypes.c_size_t, [i64]),
+            "token_logprob": (i32, [P, i32, i64, i64, i64, f32, P, P, P]),
+            "preference_loss": (i32, [P, i32, i64, i64, i64, f32, P, P, i64, P, i32, f32, f32, f32, i32, f32, P, P,
+                                      P, P, i64, P, ctypes.c_size_t, P]),
+            "policy_loss": (i32, [P, i32, i64, i64, i64, f32, P, P, P, P, P, f32, f32, f32, f32, P, P, P, i64, P,
+                                  ctypes.c_size_t, P]),
             "qlora_status_string": (ctypes.c_char_p, [i32]),
             "qlora_device_status": (i32, [i32]),
             "qlora_last_path": (i32, []),
@@ -320,6 +345,254 @@ def qlora_linear_bwd_dropout(X, dY, w: NF4Weight, A, B, scaling: float, dropout_
         float(dropout_p), int(seed), int(offset), _ptr(T), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(),
         _stream(stream)))
     return dX, dA, dB
+
+
+# --------------------------------------------------------------------------
+# 8-bit activation checkpoints
+# --------------------------------------------------------------------------
+def _need(t, name: str, dtype, *shape):
+    """t is a dense tensor of this type and shape on the current device (the pointers go to the kernels as they are)."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != shape:
+        got = f"{t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ValueError(f"{name}: {dtype} {shape} wanted, got {got}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    _on_device(t, name)
+    return t
+
+
+def _on_device(t, name: str):
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
+
+
+def _keep(stream, *tensors):
+    """Memory taken from the current stream's pool and used on `stream` goes back to it only after that use."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+@dataclass
+class Act8Tensor:
+    """An activation [M, K] kept in 8 bits: codes and one scale byte per 32 values of a row."""
+    codes: torch.Tensor    # uint8 [M, K]
+    scales: torch.Tensor   # uint8 [M, K / 32]
+    M: int
+    K: int
+    fmt: int = QLORA_ACT8_INT8
+
+    def c_struct(self) -> _Act8:
+        _need(self.codes, "codes", torch.uint8, self.M, self.K)
+        _need(self.scales, "scales", torch.uint8, self.M, self.K // QLORA_ACT8_BLOCK)
+        return _Act8(self.codes.data_ptr(), self.scales.data_ptr(), self.M, self.K, self.fmt)
+
+    @staticmethod
+    def empty(M: int, K: int, device="cuda", fmt: int = QLORA_ACT8_INT8) -> "Act8Tensor":
+        act8_sizes(M, K)
+        return Act8Tensor(torch.empty((M, K), dtype=torch.uint8, device=device),
+                          torch.empty((M, K // QLORA_ACT8_BLOCK), dtype=torch.uint8, device=device), M, K, fmt)
+
+
+def act8_sizes(M: int, K: int):
+    """(bytes of the codes, bytes of the scales) of an [M, K] checkpoint."""
+    cb, sb = ctypes.c_int64(), ctypes.c_int64()
+    _check("act8_sizes", lib().act8_sizes(M, K, ctypes.byref(cb), ctypes.byref(sb)))
+    return cb.value, sb.value
+
+
+def act8_quantize(X: torch.Tensor, fmt: int = QLORA_ACT8_INT8, out: Act8Tensor | None = None,
+                  stream=None) -> Act8Tensor:
+    """bf16 X [M, K] (device) -> 8-bit checkpoint."""
+    M, K = X.shape
+    _need(X, "X", torch.bfloat16, M, K)
+    if out is None:
+        out = Act8Tensor.empty(M, K, X.device, fmt)
+        _keep(stream, out.codes, out.scales)
+    elif (out.M, out.K) != (M, K):
+        raise ValueError(f"out: a checkpoint of {(M, K)} wanted, got {(out.M, out.K)}")
+    out.fmt = int(fmt)
+    st = out.c_struct()
+    _check("act8_quantize", lib().act8_quantize(_ptr(X), M, K, int(fmt), st.codes, st.scales, _stream(stream)))
+    return out
+
+
+def act8_dequant(x: Act8Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """8-bit checkpoint -> the bf16 tensor it stands for."""
+    if out is None:
+        out = torch.empty((x.M, x.K), dtype=torch.bfloat16, device=x.codes.device)
+        _keep(stream, out)
+    _need(out, "out", torch.bfloat16, x.M, x.K)
+    st = x.c_struct()
+    _check("act8_dequant", lib().act8_dequant(ctypes.byref(st), _ptr(out), _stream(stream)))
+    return out
+
+
+def qlora_act8_workspace_bytes(M: int, N: int, K: int, r: int, dropout: bool = False) -> int:
+    return int(lib().qlora_act8_workspace_bytes(M, N, K, r, int(dropout)))
+
+
+def act8_workspace(M: int, N: int, K: int, r: int, dropout: bool = False, device="cuda") -> torch.Tensor:
+    n = qlora_act8_workspace_bytes(M, N, K, r, dropout)
+    if n == 0:
+        raise QLoRAError("qlora_act8_workspace_bytes", -2)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def qlora_linear_bwd_act8(X: Act8Tensor, dY, w: NF4Weight, A, B, scaling: float, T=None, dX=None, dA=None, dB=None,
+                          dropout_p: float = 0.0, seed: int = 0, offset: int = 0, ws=None, stream=None):
+    """qlora_linear_bwd (dropout_p > 0: qlora_linear_bwd_dropout) from an 8-bit checkpoint of X; (dX, dA, dB)."""
+    M, K, N, r, bf = X.M, w.K, w.N, A.shape[0], torch.bfloat16
+    dev = X.codes.device
+    _need(dY, "dY", bf, M, N)
+    _need(A, "A", bf, r, K)
+    _need(B, "B", bf, N, r)
+    if T is not None:
+        _need(T, "T", bf, M, r)
+    if dX is None:
+        dX = torch.empty((M, K), dtype=bf, device=dev)
+    if dA is None:
+        dA = torch.empty((r, K), dtype=bf, device=dev)
+    if dB is None:
+        dB = torch.empty((N, r), dtype=bf, device=dev)
+    if ws is None:
+        ws = act8_workspace(M, N, K, r, dropout_p > 0, dev)
+    _keep(stream, dX, dA, dB, ws)
+    _need(dX, "dX", bf, M, K)
+    _need(dA, "dA", bf, r, K)
+    _need(dB, "dB", bf, N, r)
+    st, sx = w.c_struct(), X.c_struct()
+    _check("qlora_linear_bwd_act8", lib().qlora_linear_bwd_act8(
+        ctypes.byref(sx), _ptr(dY), ctypes.byref(st), _ptr(A), _ptr(B), r, float(scaling), float(dropout_p),
+        int(seed), int(offset), _ptr(T), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), _stream(stream)))
+    return dX, dA, dB
+
+
+# --------------------------------------------------------------------------
+# losses on logits
+# --------------------------------------------------------------------------
+_LOGITS = {torch.bfloat16: QLORA_LOGITS_BF16, torch.float32: QLORA_LOGITS_FP32}
+
+
+def _logits_args(logits, targets, name="logits"):
+    """(dtype, M, V, row pitch) of [M, V] logits whose rows are dense."""
+    if logits.dim() != 2 or logits.dtype not in _LOGITS:
+        raise ValueError(f"{name}: bf16 or fp32 [M, V] wanted, got {logits.dtype} {tuple(logits.shape)}")
+    M, V = logits.shape
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row are not adjacent")
+    ld = logits.stride(0) if M > 1 else max(V, logits.stride(0))
+    _on_device(logits, name)
+    _need(targets, "targets", torch.int64, M)
+    return _LOGITS[logits.dtype], M, V, ld
+
+
+def _grad_args(dlogits, logits, want):
+    """The gradient tensor (made when `want` and none is given), and its row pitch."""
+    if dlogits is None:
+        if not want:
+            return None, logits.shape[1]
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
+        raise ValueError(f"dlogits: {logits.dtype} {tuple(logits.shape)} wanted, got {dlogits.dtype} "
+                         f"{tuple(dlogits.shape)}")
+    if dlogits.shape[1] > 1 and dlogits.stride(1) != 1:
+        raise ValueError("dlogits: the elements of a row are not adjacent")
+    _on_device(dlogits, "dlogits")
+    M, V = dlogits.shape
+    return dlogits, dlogits.stride(0) if M > 1 else max(V, dlogits.stride(0))
+
+
+def loss_workspace_bytes(M: int) -> int:
+    return int(lib().loss_workspace_bytes(M))
+
+
+def loss_workspace(M: int, device="cuda") -> torch.Tensor:
+    n = loss_workspace_bytes(M)
+    if n == 0:
+        raise QLoRAError("loss_workspace_bytes", -2)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def token_logprob(logits: torch.Tensor, targets: torch.Tensor, logit_scale: float = 1.0, out=None,
+                  stream=None) -> torch.Tensor:
+    """fp32 [M]: log-probability of each row's target (0 where the target is outside [0, V))."""
+    dt, M, V, ld = _logits_args(logits, targets)
+    if out is None:
+        out = torch.empty(M, dtype=torch.float32, device=logits.device)
+        _keep(stream, out)
+    _need(out, "out", torch.float32, M)
+    _check("token_logprob", lib().token_logprob(_ptr(logits), dt, M, V, ld, float(logit_scale), _ptr(targets),
+                                                _ptr(out), _stream(stream)))
+    return out
+
+
+@dataclass
+class PreferenceOut:
+    loss: torch.Tensor      # fp32 scalar
+    rewards: torch.Tensor   # fp32 [2 P]
+    logp: torch.Tensor      # fp32 [M]
+    dlogits: torch.Tensor | None
+
+
+def preference_loss(logits, targets, cu_seqlens, ref_logp, beta: float, kind: int = QLORA_PREF_SIGMOID,
+                    label_smoothing: float = 0.0, margin: float = 0.0, average: bool = False,
+                    logit_scale: float = 1.0, grad_scale: float = 1.0, dlogits=None, want_grad: bool = True, ws=None,
+                    stream=None) -> PreferenceOut:
+    """Paired preference loss over packed sequences, with the gradient of the logits.
+
+    cu_seqlens int32 [2 P + 1]: pair p prefers sequence 2p to sequence 2p + 1.  ref_logp fp32 [M] or None.
+    dlogits may be the logits themselves; with want_grad=False and no dlogits, the loss alone."""
+    dt, M, V, ld = _logits_args(logits, targets)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 3 or cu_seqlens.numel() % 2 != 1:
+        raise ValueError(f"cu_seqlens: [2 P + 1] wanted, got {tuple(cu_seqlens.shape)}")
+    _need(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.numel())
+    P = cu_seqlens.numel() // 2
+    if ref_logp is not None:
+        _need(ref_logp, "ref_logp", torch.float32, M)
+    dlogits, ldd = _grad_args(dlogits, logits, want_grad)
+    dev, f32 = logits.device, torch.float32
+    loss, rewards, logp = (torch.empty(s, dtype=f32, device=dev) for s in ((), (2 * P,), (M,)))
+    if ws is None:
+        ws = loss_workspace(M, dev)
+    _keep(stream, loss, rewards, logp, dlogits, ws)
+    _check("preference_loss", lib().preference_loss(
+        _ptr(logits), dt, M, V, ld, float(logit_scale), _ptr(targets), _ptr(cu_seqlens), P, _ptr(ref_logp), int(kind),
+        float(beta), float(label_smoothing), float(margin), int(average), float(grad_scale), _ptr(loss),
+        _ptr(rewards), _ptr(logp), _ptr(dlogits), ldd, _ptr(ws), ws.numel(), _stream(stream)))
+    return PreferenceOut(loss, rewards, logp, dlogits)
+
+
+@dataclass
+class PolicyOut:
+    stats: torch.Tensor     # fp32 [4]: loss, policy term, KL, weight of the clipped rows
+    logp: torch.Tensor      # fp32 [M]
+    dlogits: torch.Tensor | None
+
+
+def policy_loss(logits, targets, advantages, weights, old_logp, ref_logp, clip_low: float = 0.2,
+                clip_high: float = 0.2, kl_coef: float = 0.0, logit_scale: float = 1.0, grad_scale: float = 1.0,
+                dlogits=None, want_grad: bool = True, ws=None, stream=None) -> PolicyOut:
+    """Clipped policy loss with a KL term, with the gradient of the logits.
+
+    advantages, weights fp32 [M]; old_logp, ref_logp fp32 [M] or None (ratio 1, no KL term).
+    dlogits may be the logits themselves; with want_grad=False and no dlogits, the loss alone."""
+    dt, M, V, ld = _logits_args(logits, targets)
+    f32, dev = torch.float32, logits.device
+    for t, name in ((advantages, "advantages"), (weights, "weights"), (old_logp, "old_logp"), (ref_logp, "ref_logp")):
+        if t is not None or name in ("advantages", "weights"):
+            _need(t, name, f32, M)
+    dlogits, ldd = _grad_args(dlogits, logits, want_grad)
+    stats, logp = torch.empty(4, dtype=f32, device=dev), torch.empty(M, dtype=f32, device=dev)
+    if ws is None:
+        ws = loss_workspace(M, dev)
+    _keep(stream, stats, logp, dlogits, ws)
+    _check("policy_loss", lib().policy_loss(
+        _ptr(logits), dt, M, V, ld, float(logit_scale), _ptr(targets), _ptr(advantages), _ptr(weights),
+        _ptr(old_logp), _ptr(ref_logp), float(clip_low), float(clip_high), float(kl_coef), float(grad_scale),
+        _ptr(stats), _ptr(logp), _ptr(dlogits), ldd, _ptr(ws), ws.numel(), _stream(stream)))
+    return PolicyOut(stats, logp, dlogits)
 
 
 def qlora_device_status(reset: bool = True) -> int:

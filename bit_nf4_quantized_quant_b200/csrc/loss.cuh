@@ -1,0 +1,620 @@
+// loss.cuh -- losses on the logits [M, V] of the output projection: the log-
+// probability of each row's target, a paired preference loss and a clipped
+// policy loss with a KL term, with the gradient of the logits.
+//
+// Row m with target y and logits l, tau = logit_scale:
+//   logp_m = tau (l_y - r) - ln S,   r = max_v l_v,   S = sum_v exp(tau (l_v - r))
+//   d logp_m / d l_v = tau (1[v = y] - p_v),   p_v = exp(tau (l_v - r)) / S
+// evaluated in base 2 (ex2 of (l - r) c, c = tau log2 e).  l - r is formed
+// before the product, so that a row of equal lowest values is uniform and
+// -inf entries give exactly 0; r = 0 stands in where nothing is above -inf.
+// Sums are fp32 per thread and merged as (maximum, sum) pairs; sums over the
+// tokens of a sequence and over rows are fp64 in a fixed order.
+//
+// Rows start at any element alignment (ld and V are arbitrary): a row is a
+// head of elements up to its first 16-byte boundary, 16-byte vectors, and a
+// tail.
+#pragma once
+#include "common.cuh"
+
+namespace qnf4 {
+namespace loss {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16-byte load without L1 allocation.  Not the read-only path: with the
+// gradient written in place other CTAs write this memory later in the kernel.
+__device__ __forceinline__ uint4 ld_v4(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+// Element types: uint16_t holds bf16 bits, float fp32.
+template <typename T> struct El;
+template <> struct El<uint16_t> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ float get(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+    static __device__ __forceinline__ uint16_t put(float x) { return (uint16_t)(pack_bf16x2(x, 0.f) & 0xffffu); }
+    static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j] = bf16lo_to_f32(w[j]);
+            f[2 * j + 1] = bf16hi_to_f32(w[j]);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+        return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                          pack_bf16x2(f[6], f[7]));
+    }
+};
+template <> struct El<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ float get(float x) { return x; }
+    static __device__ __forceinline__ float put(float x) { return x; }
+    static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
+        f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
+        f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+};
+
+// A row's elements before its first 16-byte boundary, its 16-byte vectors, and the rest.
+template <typename T>
+struct Row {
+    int head, tail;
+    int64_t nv;
+    __device__ __forceinline__ Row(const T* x, int64_t V) {
+        constexpr int N = El<T>::N;
+        const int h = (int)(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T));
+        head = (int64_t)h < V ? h : (int)V;
+        nv = (V - head) / N;
+        tail = (int)(V - head - nv * N);
+    }
+};
+
+// Running (maximum, sum of ex2((l - maximum) c)) of a set of logits.
+struct __align__(8) MS {
+    float m, s;
+};
+
+__device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.f : m; }
+
+__device__ __forceinline__ MS merge(const MS& a, const MS& b, float c) {
+    MS o;
+    o.m = fmaxf(a.m, b.m);
+    const float r = ref_of(o.m);
+    o.s = a.s * ex2((a.m - r) * c) + b.s * ex2((b.m - r) * c);
+    return o;
+}
+
+template <int N>
+__device__ __forceinline__ void add(MS& a, const float (&f)[N], float c) {
+    float bm = f[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j) bm = fmaxf(bm, f[j]);
+    if (bm > a.m) {
+        a.s *= ex2((a.m - bm) * c);
+        a.m = bm;
+    }
+    const float r = ref_of(a.m);
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) (j & 1 ? s1 : s0) += ex2((f[j] - r) * c);
+    a.s += s0 + s1;
+}
+
+__device__ __forceinline__ void add1(MS& a, float x, float c) {
+    const float f[1] = {x};
+    add(a, f, c);
+}
+
+constexpr int kRowThreads = 512;                 // largest block of the row kernels
+constexpr int kMaxZ = 8;                         // CTAs of a cluster that share a row
+
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t z;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(z));
+    return z;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void st_dsmem_f2(uint32_t addr, float a, float b) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
+}
+
+struct RowShared {
+    MS warp[kRowThreads / 32];
+    MS rank[kMaxZ];                              // written by the CTAs of the cluster
+};
+
+// (maximum, sum) of the whole row, in every thread of every CTA of the
+// cluster.  A CTA's pair is pushed into the shared memory of every other
+// one; the caller has arrived on the cluster barrier once at its start (so
+// that every CTA is known to run) and not waited yet.
+__device__ __forceinline__ MS row_total(MS v, float c, RowShared& sh, uint32_t rank, uint32_t z) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+        MS o;
+        o.m = __shfl_xor_sync(0xffffffffu, v.m, off);
+        o.s = __shfl_xor_sync(0xffffffffu, v.s, off);
+        v = merge(v, o, c);
+    }
+    if (lane == 0) sh.warp[warp] = v;
+    __syncthreads();
+    v = lane < nw ? sh.warp[lane] : MS{-INFINITY, 0.f};
+#pragma unroll
+    for (int off = kRowThreads / 64; off >= 1; off >>= 1) {
+        MS o;
+        o.m = __shfl_xor_sync(0xffffffffu, v.m, off);
+        o.s = __shfl_xor_sync(0xffffffffu, v.s, off);
+        v = merge(v, o, c);
+    }
+    v.m = __shfl_sync(0xffffffffu, v.m, 0);
+    v.s = __shfl_sync(0xffffffffu, v.s, 0);
+    if (z == 1) return v;
+    cluster_wait();                              // every CTA of the cluster has started
+    if (threadIdx.x < z) st_dsmem_f2(mapa(smem_u32(&sh.rank[rank]), threadIdx.x), v.m, v.s);
+    cluster_arrive();
+    cluster_wait();
+    MS t = sh.rank[0];
+    for (uint32_t q = 1; q < z; ++q) t = merge(t, sh.rank[q], c);
+    return t;
+}
+
+// ---------------------------------------------------------------------------
+// log-probability of the target
+// ---------------------------------------------------------------------------
+struct RowArgs {
+    const void* logits;
+    int64_t M, V, ld;
+    float tau, c;                // logit scale; logit scale * log2 e
+    const int64_t* targets;
+    float* logp;                 // [M]
+    float2* stats;               // [M] (r, log2 S), or null
+};
+
+constexpr int kUnroll = 4;
+
+// One row per cluster of z CTAs (z = 1 unless there are few rows).
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) k_token_logprob(const RowArgs a) {
+    __shared__ RowShared sh;
+    constexpr int N = El<T>::N;
+    const uint32_t rank = cluster_rank(), z = cluster_size();
+    if (z > 1) cluster_arrive();
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t row = blockIdx.x / z;
+    const int64_t y = a.targets[row];
+    if (y < 0 || y >= a.V) {
+        if (rank == 0 && threadIdx.x == 0) {
+            a.logp[row] = 0.f;
+            if (a.stats) a.stats[row] = make_float2(0.f, 0.f);
+        }
+        if (z > 1) cluster_wait();
+        return;
+    }
+    const T* x = static_cast<const T*>(a.logits) + row * a.ld;
+    const float ly = El<T>::get(x[y]);
+    const Row<T> sp(x, a.V);
+    const int64_t per = cdiv(sp.nv, z), v0 = rank * per, v1 = v0 + per < sp.nv ? v0 + per : sp.nv;
+    const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
+    const int bt = blockDim.x, tid = threadIdx.x;
+    MS acc{-INFINITY, 0.f};
+    int64_t i = v0 + tid;
+    for (; i + (kUnroll - 1) * bt < v1; i += kUnroll * bt) {
+        uint4 v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) v[u] = ld_v4(xv + i + u * bt);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            float f[N];
+            El<T>::unpack(v[u], f);
+            add(acc, f, a.c);
+        }
+    }
+    for (; i < v1; i += bt) {
+        float f[N];
+        El<T>::unpack(ld_v4(xv + i), f);
+        add(acc, f, a.c);
+    }
+    if (rank == 0) {
+        if (tid < sp.head) add1(acc, El<T>::get(x[tid]), a.c);
+        else if (tid >= 8 && tid < 8 + sp.tail) add1(acc, El<T>::get(x[a.V - sp.tail + tid - 8]), a.c);
+    }
+    const MS t = row_total(acc, a.c, sh, rank, z);
+    if (rank == 0 && tid == 0) {
+        const float r = ref_of(t.m);
+        a.logp[row] = (ly - r) * a.tau - logf(t.s);
+        if (a.stats) a.stats[row] = make_float2(r, log2f(t.s));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// gradient of sum_m d_m logp_m with respect to the logits
+// ---------------------------------------------------------------------------
+struct GradArgs {
+    const void* logits;
+    int64_t M, V, ld;
+    float tau, c;
+    const int64_t* targets;
+    const float2* stats;         // [M] of k_token_logprob
+    const float* dlogp;          // [M] (not read where the target is outside [0, V))
+    void* out;                   // may be the logits themselves (ldo == ld)
+    int64_t ldo;
+    int64_t chunks;              // per row
+};
+
+constexpr int kGradThreads = 256;
+constexpr int kGradVecs = 4;                     // 16-byte vectors per thread
+
+// One chunk of kGradThreads * kGradVecs vectors of a row per CTA, the last
+// rows first: those are what the forward pass has left in L2.
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads) k_dlogits(const GradArgs a) {
+    constexpr int N = El<T>::N;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t row = a.M - 1 - blockIdx.x / a.chunks;
+    const int64_t ch = blockIdx.x % a.chunks;
+    const T* x = static_cast<const T*>(a.logits) + row * a.ld;
+    T* o = static_cast<T*>(a.out) + row * a.ldo;
+    const int64_t y = a.targets[row];
+    const float d = (y >= 0 && y < a.V) ? a.dlogp[row] * a.tau : 0.f;
+    const float2 st = a.stats[row];
+    const int tid = threadIdx.x;
+    const int64_t cv = (int64_t)kGradThreads * kGradVecs;
+    auto one = [&](float l, int64_t v) {
+        const float p = ex2((l - st.x) * a.c - st.y);
+        return v == y ? d - d * p : -d * p;
+    };
+    if (((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) & 15) != 0) {
+        // the two rows cross 16-byte boundaries at different elements
+        const int64_t e1 = (ch + 1) * cv * N < a.V ? (ch + 1) * cv * N : a.V;
+        for (int64_t e = ch * cv * N + tid; e < e1; e += kGradThreads)
+            o[e] = El<T>::put(d == 0.f ? 0.f : one(El<T>::get(x[e]), e));
+        return;
+    }
+    const Row<T> sp(x, a.V);
+    const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
+    uint4* ov = reinterpret_cast<uint4*>(o + sp.head);
+    const int64_t i0 = ch * cv + tid;
+    if (ch == 0) {
+        const int64_t e = tid < sp.head ? tid : tid >= 8 && tid < 8 + sp.tail ? a.V - sp.tail + tid - 8 : -1;
+        if (e >= 0) o[e] = El<T>::put(d == 0.f ? 0.f : one(El<T>::get(x[e]), e));
+    }
+    if (d == 0.f) {                              // padding, or a loss that is flat here: the logits are not read
+#pragma unroll
+        for (int u = 0; u < kGradVecs; ++u)
+            if (i0 + u * kGradThreads < sp.nv) ov[i0 + u * kGradThreads] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    uint4 v[kGradVecs];
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u)
+        v[u] = i0 + u * kGradThreads < sp.nv ? ld_v4(xv + i0 + u * kGradThreads) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u) {
+        const int64_t i = i0 + u * kGradThreads;
+        if (i >= sp.nv) break;
+        float f[N];
+        El<T>::unpack(v[u], f);
+        const int64_t e0 = sp.head + i * N;
+#pragma unroll
+        for (int j = 0; j < N; ++j) f[j] = one(f[j], e0 + j);
+        ov[i] = El<T>::pack(f);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// preference loss over pairs of packed sequences
+// ---------------------------------------------------------------------------
+struct PairArgs {
+    const float* logp;           // [M]
+    const float* ref;            // [M], or null (reference-free)
+    const int64_t* targets;
+    int64_t M, V, P;
+    const int32_t* cu;           // [2 P + 1]
+    int kind, average;
+    float beta, smooth, margin, grad_scale;
+    float* loss;                 // [1]
+    float* rewards;              // [2 P]
+    float* dlogp;                // [M], or null
+};
+
+constexpr int kPairThreads = 1024, kPairCtas = 8;
+constexpr int kPairWarpTokens = 1024;            // longest pair that one warp takes
+
+struct PairShared {
+    double red[kPairThreads / 32][4];
+    double warp_loss[kPairThreads / 32];
+    double rank_loss[kPairCtas];
+    uint32_t is_long[32];
+};
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// One pair by one warp (CTA = false) or by the whole CTA; returns the pair's loss.
+template <bool CTA>
+__device__ __forceinline__ double do_pair(const PairArgs& a, int64_t p, PairShared& sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int id = CTA ? threadIdx.x : lane, n = CTA ? kPairThreads : 32;
+    // the boundaries are device data: clamped, so that no value of theirs leads out of the arrays
+    auto at = [&](int64_t i, int64_t lo) {
+        int64_t c = a.cu[i];
+        c = c < lo ? lo : c;
+        return c < a.M ? c : a.M;
+    };
+    const int64_t s0 = at(2 * p, 0), s1 = at(2 * p + 1, s0), s2 = at(2 * p + 2, s1);
+    double t[4] = {0., 0., 0., 0.};              // chosen sum, rejected sum, chosen count, rejected count
+#pragma unroll 4
+    for (int64_t i = s0 + id; i < s2; i += n) {
+        const int64_t y = a.targets[i];
+        const float lp = a.logp[i], rf = a.ref ? a.ref[i] : 0.f;
+        if (y >= 0 && y < a.V) {
+            const double d = (double)lp - (double)rf;
+            if (i < s1) { t[0] += d; t[2] += 1.; }
+            else { t[1] += d; t[3] += 1.; }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[j] = warp_sum(t[j]);
+    if (CTA) {
+        if (lane == 0)
+            for (int j = 0; j < 4; ++j) sh.red[warp][j] = t[j];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t[j] = warp_sum(sh.red[lane][j]);
+        __syncthreads();
+    }
+    const double dc = a.average && t[2] > 0. ? 1. / t[2] : 1., dr = a.average && t[3] > 0. ? 1. / t[3] : 1.;
+    const double sc = t[0] * dc, sr = t[1] * dr, delta = sc - sr;
+    const double beta = (double)a.beta, eps = (double)a.smooth;
+    const double zz = beta * delta - (double)a.margin;
+    double l, g;                                 // loss and d loss / d delta
+    if (a.kind == QLORA_PREF_SIGMOID) {
+        const double e = exp(-fabs(zz)), sp = log1p(e);
+        l = (1. - eps) * (sp + fmax(-zz, 0.)) + (eps != 0. ? eps * (sp + fmax(zz, 0.)) : 0.);
+        const double sg = zz >= 0. ? e / (1. + e) : 1. / (1. + e);      // sigmoid(-z)
+        g = beta * (eps * (1. - sg) - (1. - eps) * sg);
+    } else if (a.kind == QLORA_PREF_HINGE) {
+        l = zz < 1. ? 1. - zz : zz == zz ? 0. : zz;
+        g = zz < 1. ? -beta : 0.;
+    } else {
+        const double q = delta - 0.5 / beta;
+        l = q * q;
+        g = 2. * q;
+    }
+    if (id == 0) {
+        a.rewards[2 * p] = (float)(beta * sc);
+        a.rewards[2 * p + 1] = (float)(beta * sr);
+    }
+    if (a.dlogp) {
+        const double k = g * (double)a.grad_scale / (double)a.P;
+        const float gc = (float)(k * dc), gr = (float)(-k * dr);
+        for (int64_t i = s0 + id; i < s2; i += n) a.dlogp[i] = i < s1 ? gc : gr;
+    }
+    return l;
+}
+
+// One cluster.  CTA c owns the pairs c, c + 8, ...: short ones go to its
+// warps, long ones are taken by the whole CTA, so that neither many short nor
+// few long pairs wait on one warp; the assignment and so every sum's order is
+// fixed.  Rows outside every sequence get gradient 0.
+__global__ void __launch_bounds__(kPairThreads) k_preference(const PairArgs a) {
+    __shared__ PairShared sh;
+    const uint32_t rank = cluster_rank();
+    cluster_arrive();
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    double acc = 0.;
+    for (int64_t base = 0; base * kPairCtas + rank < a.P; base += kPairThreads) {
+        const int64_t mine = (base + tid) * kPairCtas + rank;
+        bool lng = false;
+        if (mine < a.P) lng = (int64_t)a.cu[2 * mine + 2] - a.cu[2 * mine] > kPairWarpTokens;
+        const uint32_t bits = __ballot_sync(0xffffffffu, lng);
+        if (lane == 0) sh.is_long[warp] = bits;
+        __syncthreads();
+        for (int j = 0; j < 32; ++j) {
+            const int64_t p = (base + 32 * j + warp) * kPairCtas + rank;
+            if (p >= a.P) break;
+            if (!((sh.is_long[j] >> warp) & 1u)) acc += do_pair<false>(a, p, sh);
+        }
+        for (int j = 0; j < 32; ++j)
+            for (uint32_t b = sh.is_long[j]; b; b &= b - 1) {
+                const int64_t p = (base + 32 * j + __ffs(b) - 1) * kPairCtas + rank;
+                const double l = do_pair<true>(a, p, sh);
+                if (warp == 0) acc += l;
+            }
+        __syncthreads();
+    }
+    if (a.dlogp) {
+        int64_t lo = a.cu[0], hi = a.cu[2 * a.P];
+        lo = lo < 0 ? 0 : lo < a.M ? lo : a.M;
+        hi = hi < lo ? lo : hi < a.M ? hi : a.M;
+        for (int64_t i = (int64_t)rank * kPairThreads + tid; i < lo + a.M - hi; i += kPairThreads * kPairCtas)
+            a.dlogp[i < lo ? i : hi + i - lo] = 0.f;
+    }
+    if (lane == 0) sh.warp_loss[warp] = acc;
+    __syncthreads();
+    cluster_wait();
+    if (warp == 0) {
+        const double v = warp_sum(sh.warp_loss[lane]);
+        if (lane == 0)
+            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(mapa(smem_u32(&sh.rank_loss[rank]), 0)), "d"(v)
+                         : "memory");
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (rank == 0 && tid == 0) {
+        double v = 0.;
+        for (int q = 0; q < kPairCtas; ++q) v += sh.rank_loss[q];
+        a.loss[0] = (float)(v / (double)a.P);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// clipped policy loss with a KL term
+// ---------------------------------------------------------------------------
+struct PolicyArgs {
+    const void* logits;
+    int64_t M, V, ld;
+    float tau, c;
+    const int64_t* targets;
+    const float* old_logp;       // [M], or null: the ratio is 1 (its gradient stays)
+    const float* ref_logp;       // [M], or null: no KL term
+    const float* adv;            // [M]
+    const float* weight;         // [M]; 0: the row takes no part
+    float lo, hi, kl, grad_scale;
+    float* logp;                 // [M]
+    float4* part;                // [M] weighted (loss, policy, kl, clipped)
+    void* out;                   // gradient, or null; may be the logits themselves (ldo == ld)
+    int64_t ldo;
+};
+
+// A row's gradient depends on that row alone, so each row is read once, held
+// in registers (NV vectors per thread of a cluster of z CTAs), and its
+// gradient written: the 2 M V elements that cannot be done without.
+template <typename T, int NV>
+__global__ void __launch_bounds__(kRowThreads, NV >= 16 ? 1 : 2) k_policy(const PolicyArgs a) {
+    __shared__ RowShared sh;
+    constexpr int N = El<T>::N;
+    const uint32_t rank = cluster_rank(), z = cluster_size();
+    if (z > 1) cluster_arrive();
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t row = blockIdx.x / z;
+    const int bt = blockDim.x, tid = threadIdx.x;
+    const int64_t y = a.targets[row];
+    const float w = a.weight[row];
+    const bool live = y >= 0 && y < a.V && w != 0.f;
+    const T* x = static_cast<const T*>(a.logits) + row * a.ld;
+    T* o = static_cast<T*>(a.out) + row * a.ldo;
+    const Row<T> sp(x, a.V);
+    const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
+    const int64_t per = cdiv(sp.nv, z), v0 = rank * per, v1 = v0 + per < sp.nv ? v0 + per : sp.nv;
+    // the one element of the head or the tail that this thread holds
+    const int64_t e1 = rank != 0 ? -1 : tid < sp.head ? tid
+                     : tid >= 8 && tid < 8 + sp.tail ? a.V - sp.tail + tid - 8 : -1;
+
+    uint4 v[NV];
+    float x1 = -INFINITY, g = 0.f, r = 0.f, ls2 = 0.f;
+    if (live) {
+        const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
+        const int64_t i0 = v0 + tid;
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+            if (i0 + u * bt < v1) v[u] = ld_v4(xv + i0 + u * bt);
+        if (e1 >= 0) x1 = El<T>::get(x[e1]);
+        const float ly = El<T>::get(x[y]);
+        MS acc{-INFINITY, 0.f};
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+            if (i0 + u * bt < v1) {
+                float f[N];
+                El<T>::unpack(v[u], f);
+                add(acc, f, a.c);
+            }
+        if (e1 >= 0) add1(acc, x1, a.c);
+        const MS t = row_total(acc, a.c, sh, rank, z);
+        r = ref_of(t.m);
+        ls2 = log2f(t.s);
+        const float lp = (ly - r) * a.tau - logf(t.s);
+        const float A = a.adv[row];
+        const float rho = a.old_logp ? expf(lp - a.old_logp[row]) : 1.f;
+        const float free_ = rho * A, held = fminf(fmaxf(rho, a.lo), a.hi) * A;
+        const bool clipped = held < free_;
+        const float d = a.ref_logp ? a.ref_logp[row] - lp : 0.f;
+        g = w * ((clipped ? 0.f : -free_) - (a.ref_logp ? a.kl * expm1f(d) : 0.f)) * a.grad_scale * a.tau;
+        if (rank == 0 && tid == 0) {
+            const float pol = -(clipped ? held : free_);
+            const float kl = a.ref_logp ? expm1f(d) - d : 0.f;
+            a.logp[row] = lp;
+            a.part[row] = make_float4(w * (pol + a.kl * kl), w * pol, w * kl, clipped ? w : 0.f);
+        }
+    } else {
+        if (z > 1) cluster_wait();
+        if (rank == 0 && tid == 0) {
+            a.logp[row] = 0.f;
+            a.part[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    if (a.out == nullptr) return;
+    auto one = [&](float l, int64_t e) {
+        const float p = ex2((l - r) * a.c - ls2);
+        return e == y ? g - g * p : -g * p;
+    };
+    const int64_t i0 = v0 + tid;
+    uint4* ov = reinterpret_cast<uint4*>(o + sp.head);
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const int64_t i = i0 + u * bt;
+        if (i < v1) {
+            float f[N];
+            const int64_t e0 = sp.head + i * N;
+            if (g != 0.f) {
+                El<T>::unpack(v[u], f);
+#pragma unroll
+                for (int j = 0; j < N; ++j) f[j] = one(f[j], e0 + j);
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j) f[j] = 0.f;
+            }
+            if (same) {
+                ov[i] = El<T>::pack(f);
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j) o[e0 + j] = El<T>::put(f[j]);
+            }
+        }
+    }
+    if (e1 >= 0) o[e1] = El<T>::put(g != 0.f ? one(x1, e1) : 0.f);
+}
+
+constexpr int kFinishThreads = 1024;
+
+// stats[j] = sum over rows of component j, fp64 in a fixed order
+__global__ void __launch_bounds__(kFinishThreads) k_policy_finish(const float4* part, int64_t M, float* stats) {
+    __shared__ double s[kFinishThreads / 32][4];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    double t[4] = {0., 0., 0., 0.};
+#pragma unroll 4
+    for (int64_t i = tid; i < M; i += kFinishThreads) {
+        const float4 p = part[i];
+        t[0] += p.x; t[1] += p.y; t[2] += p.z; t[3] += p.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        t[j] = warp_sum(t[j]);
+        if (lane == 0) s[warp][j] = t[j];
+    }
+    __syncthreads();
+    if (warp < 4) {
+        const double v = warp_sum(s[lane][warp]);
+        if (lane == 0) stats[warp] = (float)v;
+    }
+}
+
+}  // namespace loss
+}  // namespace qnf4

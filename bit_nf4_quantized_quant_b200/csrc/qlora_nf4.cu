@@ -22,6 +22,8 @@
 #include "merge.cuh"
 #include "adamw8.cuh"
 #include "skinny.cuh"
+#include "act8.cuh"
+#include "loss.cuh"
 
 using namespace qnf4;
 
@@ -971,6 +973,96 @@ int launch_dropout_x(const uint16_t* X, int64_t M, int64_t K, uint8_t* dst, uint
     return launch_status();
 }
 
+// ---------------------------------------------------------------------------
+// 8-bit activation checkpoints
+// ---------------------------------------------------------------------------
+int check_act8(const act8_tensor* x) {
+    if (!x || !x->codes || !x->scales) return QLORA_ERR_NULL;
+    if (x->fmt != QLORA_ACT8_INT8 && x->fmt != QLORA_ACT8_E4M3) return QLORA_ERR_VALUE;
+    if (act8_sizes(x->M, x->K, nullptr, nullptr) != QLORA_OK) return QLORA_ERR_SHAPE;
+    if (!aligned16(x->codes)) return QLORA_ERR_ALIGN;
+    return QLORA_OK;
+}
+
+int launch_act8_dequant(const act8_tensor* x, uint16_t* out, int sms, cudaStream_t st) {
+    const int64_t n8 = x->M * x->K / 8;
+    const int grid = grid_for(n8, act8::kWarpChunks * (act8::kThreads / 32), sms, 8);
+    if (x->fmt == QLORA_ACT8_E4M3)
+        act8::k_act8_dequant<true><<<grid, act8::kThreads, 0, st>>>(x->codes, x->scales, n8, out);
+    else
+        act8::k_act8_dequant<false><<<grid, act8::kThreads, 0, st>>>(x->codes, x->scales, n8, out);
+    note_launch();
+    return launch_status();
+}
+
+// ---------------------------------------------------------------------------
+// Losses on logits
+// ---------------------------------------------------------------------------
+size_t logit_bytes(int dtype) { return dtype == QLORA_LOGITS_FP32 ? 4 : 2; }
+
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// The checks that every entry point on logits shares.
+int check_logits(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float tau, const int64_t* targets) {
+    if (!logits || !targets) return QLORA_ERR_NULL;
+    if (dtype != QLORA_LOGITS_BF16 && dtype != QLORA_LOGITS_FP32) return QLORA_ERR_VALUE;
+    if (M <= 0 || V <= 0 || V > QLORA_MAX_VOCAB || ld < V || M > ((int64_t)1 << 24) || ld > ((int64_t)1 << 32))
+        return QLORA_ERR_SHAPE;
+    if (!(tau > 0.f) || !std::isfinite(tau) || !std::isfinite(tau * loss::kLog2e)) return QLORA_ERR_VALUE;
+    if (!aligned_to(logits, logit_bytes(dtype)) || !aligned_to(targets, 8)) return QLORA_ERR_ALIGN;
+    return QLORA_OK;
+}
+
+template <typename... KArgs, typename... Args>
+int launch_rows(void (*kern)(KArgs...), int64_t rows, int z, int threads, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(rows * z));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)z; at[1].val.clusterDim.y = 1; at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = z > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    note_launch();
+    return e == cudaSuccess ? QLORA_OK : QLORA_ERR_LAUNCH;
+}
+
+int row_threads(int64_t nv) { return nv <= 128 ? 128 : nv <= 1024 ? 256 : loss::kRowThreads; }
+
+int launch_logprob(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float tau, const int64_t* targets,
+                   float* logp, float2* stats, int sms, cudaStream_t st) {
+    loss::RowArgs a{};
+    a.logits = logits; a.M = M; a.V = V; a.ld = ld; a.tau = tau; a.c = tau * loss::kLog2e;
+    a.targets = targets; a.logp = logp; a.stats = stats;
+    const int64_t nv = V * (int64_t)logit_bytes(dtype) / 16;
+    const int threads = row_threads(nv);
+    // a row is split over a cluster while the rows alone would not fill the SMs
+    int z = 1;
+    while (z < loss::kMaxZ && M * z * 2 <= 4 * (int64_t)sms && nv >= 2 * z * threads) z *= 2;
+    return dtype == QLORA_LOGITS_FP32 ? launch_rows(loss::k_token_logprob<float>, M, z, threads, st, a)
+                                      : launch_rows(loss::k_token_logprob<uint16_t>, M, z, threads, st, a);
+}
+
+template <typename T>
+int launch_policy(const loss::PolicyArgs& a, int sms, cudaStream_t st) {
+    const int64_t nv = a.V * (int64_t)sizeof(T) / 16;
+    const int threads = row_threads(nv);
+    int z = 1;
+    while (z < loss::kMaxZ &&
+           (nv > (int64_t)z * threads * 8 || (a.M * z * 2 <= 2 * (int64_t)sms && nv >= 2 * z * threads)))
+        z *= 2;
+    const int64_t per = cdiv(nv, z);
+    if (per <= threads) return launch_rows(loss::k_policy<T, 1>, a.M, z, threads, st, a);
+    if (per <= 2 * threads) return launch_rows(loss::k_policy<T, 2>, a.M, z, threads, st, a);
+    if (per <= 4 * threads) return launch_rows(loss::k_policy<T, 4>, a.M, z, threads, st, a);
+    if (per <= 8 * threads) return launch_rows(loss::k_policy<T, 8>, a.M, z, threads, st, a);
+    return launch_rows(loss::k_policy<T, 16>, a.M, z, threads, st, a);
+}
+
 }  // namespace
 
 // ===========================================================================
@@ -1177,27 +1269,35 @@ static int fwd_impl(const qlora_bf16* X, int64_t M, const nf4dq_weight* w, const
 }
 
 // The backward; with dp the LoRA branch reads the dropped copy of X and the
-// LoRA term of dX is masked (keep * c).
-static int bwd_impl(const qlora_bf16* X, const qlora_bf16* dY, int64_t M, const nf4dq_weight* w,
-                    const qlora_bf16* A, const qlora_bf16* B, int r, float scaling, const qlora_bf16* T,
-                    qlora_bf16* dX, qlora_bf16* dA, qlora_bf16* dB, void* ws, size_t ws_bytes,
+// LoRA term of dX is masked (keep * c).  With x8, X is that checkpoint.
+static int bwd_impl(const qlora_bf16* X, const act8_tensor* x8, const qlora_bf16* dY, int64_t M,
+                    const nf4dq_weight* w, const qlora_bf16* A, const qlora_bf16* B, int r, float scaling,
+                    const qlora_bf16* T, qlora_bf16* dX, qlora_bf16* dA, qlora_bf16* dB, void* ws, size_t ws_bytes,
                     qlora_stream_t stream, const drop::Params* dp) {
-    if (!X || !dY || !A || !B || !dX || !dA || !dB) return QLORA_ERR_NULL;
+    if ((!X && !x8) || !dY || !A || !B || !dX || !dA || !dB) return QLORA_ERR_NULL;
     int rc = validate_weight(w);
     if (rc != QLORA_OK) return rc;
+    if (x8 && (x8->M != M || x8->K != w->K)) return QLORA_ERR_SHAPE;
     if (M <= 0 || M > ((int64_t)1 << 31)) return QLORA_ERR_SHAPE;
     if (r < 1 || r > QLORA_MAX_RANK) return QLORA_ERR_RANK;
     if (!std::isfinite(scaling)) return QLORA_ERR_VALUE;
-    if (!aligned16(X) || !aligned16(dY) || !aligned16(A) || !aligned16(dX)) return QLORA_ERR_ALIGN;
+    if ((X && !aligned16(X)) || !aligned16(dY) || !aligned16(A) || !aligned16(dX)) return QLORA_ERR_ALIGN;
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return ws ? QLORA_ERR_ALIGN : QLORA_ERR_WORKSPACE;
     int sms = 0;
     rc = check_device(&sms);
     if (rc != QLORA_OK) return rc;
     const int64_t N = w->N, K = w->K;
     const Plan p = make_plan(M, N, K, r, 148);
-    if (ws_bytes < p.total + (dp ? dropout_bytes(M, K) : 0)) return QLORA_ERR_WORKSPACE;
+    const size_t xb = align256((size_t)M * (size_t)K * 2);       // a restored copy of X
+    if (ws_bytes < p.total + (dp ? dropout_bytes(M, K) : 0) + (x8 ? xb : 0)) return QLORA_ERR_WORKSPACE;
     cudaStream_t st = (cudaStream_t)stream;
     uint8_t* wsb = static_cast<uint8_t*>(ws);
+    if (x8) {
+        uint16_t* xr = reinterpret_cast<uint16_t*>(wsb + p.total + (dp ? dropout_bytes(M, K) : 0));
+        rc = launch_act8_dequant(x8, xr, sms, st);
+        if (rc != QLORA_OK) return rc;
+        X = xr;
+    }
     const uint16_t* Xl = X;
     uint16_t* mask = nullptr;
     if (dp) {
@@ -1336,7 +1436,7 @@ int qlora_linear_bwd(const qlora_bf16* X, const qlora_bf16* dY, int64_t M, const
                      const qlora_bf16* A, const qlora_bf16* B, int r, float scaling, const qlora_bf16* T,
                      qlora_bf16* dX, qlora_bf16* dA, qlora_bf16* dB, void* ws, size_t ws_bytes,
                      qlora_stream_t stream) {
-    return bwd_impl(X, dY, M, w, A, B, r, scaling, T, dX, dA, dB, ws, ws_bytes, stream, nullptr);
+    return bwd_impl(X, nullptr, dY, M, w, A, B, r, scaling, T, dX, dA, dB, ws, ws_bytes, stream, nullptr);
 }
 
 size_t qlora_dropout_workspace_bytes(int64_t M, int64_t N, int64_t K, int r) {
@@ -1361,7 +1461,156 @@ int qlora_linear_bwd_dropout(const qlora_bf16* X, const qlora_bf16* dY, int64_t 
     drop::Params d{};
     const int rc = dropout_params(dropout_p, seed, offset, &d);
     if (rc != QLORA_OK) return rc;
-    return bwd_impl(X, dY, M, w, A, B, r, scaling, T, dX, dA, dB, ws, ws_bytes, stream, &d);
+    return bwd_impl(X, nullptr, dY, M, w, A, B, r, scaling, T, dX, dA, dB, ws, ws_bytes, stream, &d);
+}
+
+int act8_sizes(int64_t M, int64_t K, int64_t* code_bytes, int64_t* scale_bytes) {
+    if (M <= 0 || K <= 0 || (K % kBlock) != 0 || M > ((int64_t)1 << 40) / K) return QLORA_ERR_SHAPE;
+    if (code_bytes) *code_bytes = M * K;
+    if (scale_bytes) *scale_bytes = M * K / QLORA_ACT8_BLOCK;
+    return QLORA_OK;
+}
+
+int act8_quantize(const qlora_bf16* X, int64_t M, int64_t K, int fmt, uint8_t* codes, uint8_t* scales,
+                  qlora_stream_t stream) {
+    if (!X) return QLORA_ERR_NULL;
+    const act8_tensor x{codes, scales, M, K, fmt};
+    int rc = check_act8(&x);
+    if (rc != QLORA_OK) return rc;
+    if (!aligned16(X)) return QLORA_ERR_ALIGN;
+    int sms = 0;
+    rc = check_device(&sms);
+    if (rc != QLORA_OK) return rc;
+    const int64_t n8 = M * K / 8;
+    const int grid = grid_for(n8, act8::kWarpChunks * (act8::kThreads / 32), sms, 8);
+    if (fmt == QLORA_ACT8_E4M3)
+        act8::k_act8_quantize<true><<<grid, act8::kThreads, 0, (cudaStream_t)stream>>>(X, n8, codes, scales);
+    else
+        act8::k_act8_quantize<false><<<grid, act8::kThreads, 0, (cudaStream_t)stream>>>(X, n8, codes, scales);
+    note_launch();
+    return launch_status();
+}
+
+int act8_dequant(const act8_tensor* x, qlora_bf16* X_out, qlora_stream_t stream) {
+    if (!X_out) return QLORA_ERR_NULL;
+    int rc = check_act8(x);
+    if (rc != QLORA_OK) return rc;
+    if (!aligned16(X_out)) return QLORA_ERR_ALIGN;
+    int sms = 0;
+    rc = check_device(&sms);
+    if (rc != QLORA_OK) return rc;
+    return launch_act8_dequant(x, X_out, sms, (cudaStream_t)stream);
+}
+
+size_t qlora_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int r, int dropout) {
+    const size_t b = dropout ? qlora_dropout_workspace_bytes(M, N, K, r) : qlora_workspace_bytes(M, N, K, r);
+    return b == 0 ? 0 : b + align256((size_t)M * (size_t)K * 2);
+}
+
+int qlora_linear_bwd_act8(const act8_tensor* X, const qlora_bf16* dY, const nf4dq_weight* w, const qlora_bf16* A,
+                          const qlora_bf16* B, int r, float scaling, float dropout_p, uint64_t seed, uint64_t offset,
+                          const qlora_bf16* T, qlora_bf16* dX, qlora_bf16* dA, qlora_bf16* dB, void* ws,
+                          size_t ws_bytes, qlora_stream_t stream) {
+    int rc = check_act8(X);
+    if (rc != QLORA_OK) return rc;
+    drop::Params d{};
+    rc = dropout_params(dropout_p, seed, offset, &d);
+    if (rc != QLORA_OK) return rc;
+    return bwd_impl(nullptr, X, dY, X->M, w, A, B, r, scaling, T, dX, dA, dB, ws, ws_bytes, stream,
+                    dropout_p > 0.f ? &d : nullptr);
+}
+
+int token_logprob(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float logit_scale,
+                  const int64_t* targets, float* logp, qlora_stream_t stream) {
+    if (!logp) return QLORA_ERR_NULL;
+    int rc = check_logits(logits, dtype, M, V, ld, logit_scale, targets);
+    if (rc != QLORA_OK) return rc;
+    if (!aligned_to(logp, 4)) return QLORA_ERR_ALIGN;
+    int sms = 0;
+    rc = check_device(&sms);
+    if (rc != QLORA_OK) return rc;
+    return launch_logprob(logits, dtype, M, V, ld, logit_scale, targets, logp, nullptr, sms, (cudaStream_t)stream);
+}
+
+size_t loss_workspace_bytes(int64_t M) { return M <= 0 || M > ((int64_t)1 << 24) ? 0 : align256((size_t)M * 16); }
+
+int preference_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float logit_scale,
+                    const int64_t* targets, const int32_t* cu_seqlens, int64_t P, const float* ref_logp, int kind,
+                    float beta, float label_smoothing, float margin, int average, float grad_scale, float* loss,
+                    float* rewards, float* logp, void* dlogits, int64_t ldd, void* ws, size_t ws_bytes,
+                    qlora_stream_t stream) {
+    if (!cu_seqlens || !loss || !rewards || !logp) return QLORA_ERR_NULL;
+    int rc = check_logits(logits, dtype, M, V, ld, logit_scale, targets);
+    if (rc != QLORA_OK) return rc;
+    if (P <= 0 || P > ((int64_t)1 << 24) || (dlogits && ldd < V) || ldd > ((int64_t)1 << 32)) return QLORA_ERR_SHAPE;
+    if (kind != QLORA_PREF_SIGMOID && kind != QLORA_PREF_HINGE && kind != QLORA_PREF_IPO) return QLORA_ERR_VALUE;
+    if (!std::isfinite(beta) || !(beta > 0.f) || !std::isfinite(margin) || !std::isfinite(grad_scale) ||
+        !(label_smoothing >= 0.f && label_smoothing <= 1.f) ||
+        (kind != QLORA_PREF_SIGMOID && label_smoothing != 0.f) || (kind == QLORA_PREF_IPO && margin != 0.f))
+        return QLORA_ERR_VALUE;
+    if (!aligned_to(cu_seqlens, 4) || (ref_logp && !aligned_to(ref_logp, 4)) || !aligned_to(loss, 4) ||
+        !aligned_to(rewards, 4) || !aligned_to(logp, 4) || (dlogits && !aligned_to(dlogits, logit_bytes(dtype))))
+        return QLORA_ERR_ALIGN;
+    if (!ws) return QLORA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return QLORA_ERR_ALIGN;
+    if (ws_bytes < loss_workspace_bytes(M)) return QLORA_ERR_WORKSPACE;
+    // the gradient's chunks of a row
+    const int64_t N = 16 / (int64_t)logit_bytes(dtype);
+    const int64_t chunks = cdiv(cdiv(V, N), (int64_t)loss::kGradThreads * loss::kGradVecs);
+    if (M * chunks > 0x7fffffffLL) return QLORA_ERR_SHAPE;
+    int sms = 0;
+    rc = check_device(&sms);
+    if (rc != QLORA_OK) return rc;
+    cudaStream_t st = (cudaStream_t)stream;
+    float2* stats = static_cast<float2*>(ws);
+    float* dlogp = reinterpret_cast<float*>(stats + M);
+    rc = launch_logprob(logits, dtype, M, V, ld, logit_scale, targets, logp, stats, sms, st);
+    if (rc != QLORA_OK) return rc;
+    loss::PairArgs a{};
+    a.logp = logp; a.ref = ref_logp; a.targets = targets; a.M = M; a.V = V; a.P = P; a.cu = cu_seqlens;
+    a.kind = kind; a.average = average != 0; a.beta = beta; a.smooth = label_smoothing; a.margin = margin;
+    a.grad_scale = grad_scale; a.loss = loss; a.rewards = rewards; a.dlogp = dlogits ? dlogp : nullptr;
+    rc = launch_rows(loss::k_preference, 1, loss::kPairCtas, loss::kPairThreads, st, a);
+    if (rc != QLORA_OK || !dlogits) return rc;
+    loss::GradArgs g{};
+    g.logits = logits; g.M = M; g.V = V; g.ld = ld; g.tau = logit_scale; g.c = logit_scale * loss::kLog2e;
+    g.targets = targets; g.stats = stats; g.dlogp = dlogp; g.out = dlogits; g.ldo = ldd; g.chunks = chunks;
+    return dtype == QLORA_LOGITS_FP32
+               ? launch_rows(loss::k_dlogits<float>, M * chunks, 1, loss::kGradThreads, st, g)
+               : launch_rows(loss::k_dlogits<uint16_t>, M * chunks, 1, loss::kGradThreads, st, g);
+}
+
+int policy_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float logit_scale,
+                const int64_t* targets, const float* advantages, const float* weights, const float* old_logp,
+                const float* ref_logp, float clip_low, float clip_high, float kl_coef, float grad_scale, float* stats,
+                float* logp, void* dlogits, int64_t ldd, void* ws, size_t ws_bytes, qlora_stream_t stream) {
+    if (!advantages || !weights || !stats || !logp) return QLORA_ERR_NULL;
+    int rc = check_logits(logits, dtype, M, V, ld, logit_scale, targets);
+    if (rc != QLORA_OK) return rc;
+    if ((dlogits && ldd < V) || ldd > ((int64_t)1 << 32)) return QLORA_ERR_SHAPE;
+    if (!(clip_low >= 0.f && clip_low <= 1.f) || !(clip_high >= 0.f) || !std::isfinite(clip_high) ||
+        !std::isfinite(kl_coef) || !std::isfinite(grad_scale))
+        return QLORA_ERR_VALUE;
+    if (!aligned_to(advantages, 4) || !aligned_to(weights, 4) || (old_logp && !aligned_to(old_logp, 4)) ||
+        (ref_logp && !aligned_to(ref_logp, 4)) || !aligned_to(stats, 4) || !aligned_to(logp, 4) ||
+        (dlogits && !aligned_to(dlogits, logit_bytes(dtype))))
+        return QLORA_ERR_ALIGN;
+    if (!ws) return QLORA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return QLORA_ERR_ALIGN;
+    if (ws_bytes < loss_workspace_bytes(M)) return QLORA_ERR_WORKSPACE;
+    int sms = 0;
+    rc = check_device(&sms);
+    if (rc != QLORA_OK) return rc;
+    cudaStream_t st = (cudaStream_t)stream;
+    loss::PolicyArgs a{};
+    a.logits = logits; a.M = M; a.V = V; a.ld = ld; a.tau = logit_scale; a.c = logit_scale * loss::kLog2e;
+    a.targets = targets; a.old_logp = old_logp; a.ref_logp = ref_logp; a.adv = advantages; a.weight = weights;
+    a.lo = 1.f - clip_low; a.hi = 1.f + clip_high; a.kl = kl_coef; a.grad_scale = grad_scale;
+    a.logp = logp; a.part = static_cast<float4*>(ws); a.out = dlogits; a.ldo = ldd;
+    rc = dtype == QLORA_LOGITS_FP32 ? launch_policy<float>(a, sms, st) : launch_policy<uint16_t>(a, sms, st);
+    if (rc != QLORA_OK) return rc;
+    return launch_pdl(loss::k_policy_finish, dim3(1), dim3(loss::kFinishThreads), 0, st, (const float4*)a.part, M,
+                      stats);
 }
 
 

@@ -273,6 +273,127 @@ QLORA_API int qlora_linear_bwd_dropout(const qlora_bf16* X, const qlora_bf16* dY
                                        qlora_bf16* dX, qlora_bf16* dA, qlora_bf16* dB, void* ws, size_t ws_bytes,
                                        qlora_stream_t stream);
 
+/* 8-bit activation checkpoints (no counterpart on the pages, which only name
+ * gradient checkpointing).  The input X [M, K] of a linear layer is kept
+ * between its forward and its backward as one byte per value and one scale
+ * byte per QLORA_ACT8_BLOCK consecutive values of a row (8.25 bits per value
+ * instead of 16).
+ *   codes  [M, K]       one byte per value: a two's complement integer in
+ *                       [-127, 127] (INT8) or an FP8 E4M3 code (E4M3)
+ *   scales [M, K / 32]  one byte s per block: the scale is 2^(s - 127)
+ *   value               code * 2^(s - 127); s = 255: every value is NaN
+ * act8_quantize: with amax = 1.m * 2^x the block's largest magnitude,
+ * s - 127 = max(x - 6, -127) for INT8 and, for E4M3, the smallest exponent
+ * >= -127 with amax / 2^(s - 127) <= 448 (x - 8, or x - 7 where 1.m > 1.75);
+ * code = value / 2^(s - 127) rounded to the nearest code, ties to even
+ * (INT8: 127.5 gives 127).  So an INT8 value is off by at most amax / 128 (half a
+ * step: 2^(x - 7)), an E4M3 value by at most 2^-4 of itself or, below
+ * 2^(s - 133), by 2^(s - 137).  A block of zeros gets s = 0, a block that
+ * holds an infinity or a NaN s = 255.  Every other step is exact: the values
+ * that act8_quantize's codes stand for are bf16 numbers, and act8_dequant
+ * writes them.
+ * act8_sizes gives the bytes of both arrays (host only; either pointer may be
+ * NULL).  Requires K % 64 == 0; X, X_out and codes 16-byte aligned. */
+#define QLORA_ACT8_BLOCK 32
+#define QLORA_ACT8_INT8 0
+#define QLORA_ACT8_E4M3 1
+typedef struct act8_tensor {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    int64_t M;
+    int64_t K;
+    int32_t fmt;                /* QLORA_ACT8_INT8 or QLORA_ACT8_E4M3 */
+} act8_tensor;
+QLORA_API int act8_sizes(int64_t M, int64_t K, int64_t* code_bytes, int64_t* scale_bytes);
+QLORA_API int act8_quantize(const qlora_bf16* X, int64_t M, int64_t K, int fmt, uint8_t* codes, uint8_t* scales,
+                            qlora_stream_t stream);
+QLORA_API int act8_dequant(const act8_tensor* x, qlora_bf16* X_out, qlora_stream_t stream);
+
+/* The backward of qlora_linear_fwd (dropout_p = 0) or
+ * qlora_linear_fwd_dropout (0 < dropout_p < 1, with that forward's seed and
+ * offset) from a checkpoint of its input: dX, dA and dB are bit for bit those
+ * of qlora_linear_bwd / qlora_linear_bwd_dropout on the tensor that
+ * act8_dequant writes.  X enters dA and, where T is NULL, T; dX does not
+ * depend on it, and with the forward's T_out neither does dB, so that only
+ * dA sees the 8-bit rounding.  M and K are the checkpoint's (K must be the
+ * weight's: else QLORA_ERR_SHAPE).  ws: at least
+ * qlora_act8_workspace_bytes(M, N, K, r, dropout_p > 0) bytes, 256-byte
+ * aligned.  Other arguments, layouts and errors: qlora_linear_bwd_dropout. */
+QLORA_API size_t qlora_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int r, int dropout);
+QLORA_API int qlora_linear_bwd_act8(const act8_tensor* X, const qlora_bf16* dY, const nf4dq_weight* w,
+                                    const qlora_bf16* A, const qlora_bf16* B, int r, float scaling, float dropout_p,
+                                    uint64_t seed, uint64_t offset, const qlora_bf16* T, qlora_bf16* dX,
+                                    qlora_bf16* dA, qlora_bf16* dB, void* ws, size_t ws_bytes, qlora_stream_t stream);
+
+/* Losses on the logits [M, V] of the output projection (no counterpart on the
+ * pages, where the loss is the trainer's).  Their gradient is the dY of that
+ * projection's qlora_linear_bwd.  Common to the three entry points:
+ *   - logits: bf16 or fp32 (dtype), rows ld >= V elements apart, aligned to
+ *     their element only; 1 <= V <= QLORA_MAX_VOCAB, 1 <= M <= 2^24.
+ *   - targets [M] int64.  A row whose target is outside [0, V) takes no part:
+ *     its logits are not read, its logp is 0, its gradient row is zero.
+ *   - logp_m = tau l_y - ln sum_v exp(tau l_v), tau = logit_scale > 0, in fp32.
+ *     Logits of -inf have probability 0; a row that holds a NaN or +inf, or
+ *     nothing above -inf, gives NaN.
+ *   - dlogits [M, V], rows ldd apart, of the logits' type, or NULL for the
+ *     loss alone; columns beyond V are not written.  It may be the logits
+ *     themselves (same pointer, ldd = ld); otherwise the two must not overlap.
+ *     It is grad_scale times the gradient of the loss.
+ *   - ws: at least loss_workspace_bytes(M) bytes, 256-byte aligned; calls that
+ *     overlap on the GPU need separate ones.
+ *   - sums over tokens are fp64 in a fixed order: results repeat bit for bit. */
+#define QLORA_LOGITS_BF16 0
+#define QLORA_LOGITS_FP32 1
+#define QLORA_MAX_VOCAB (1 << 18)
+QLORA_API size_t loss_workspace_bytes(int64_t M);
+
+/* logp [M] alone, e.g. of a reference or behaviour policy. */
+QLORA_API int token_logprob(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float logit_scale,
+                            const int64_t* targets, float* logp, qlora_stream_t stream);
+
+/* Preference loss over P pairs of packed sequences: sequence i is rows
+ * [cu_seqlens[i], cu_seqlens[i + 1]), pair p prefers sequence 2p to 2p + 1;
+ * cu_seqlens [2P + 1] int32, ascending (device data: values are clamped to
+ * [0, M] and to the one before).  Rows in no sequence get gradient 0.
+ *   S_i     = sum over the sequence's rows with a target of logp - ref_logp
+ *             (ref_logp NULL: of logp), divided by their number with
+ *             average != 0 (a sequence without any: 0)
+ *   Delta_p = S_2p - S_2p+1,   z_p = beta Delta_p - margin
+ *   SIGMOID: -(1 - eps) ln sigma(z) - eps ln sigma(-z), eps = label_smoothing
+ *   HINGE:   max(0, 1 - z)          IPO: (Delta - 1 / (2 beta))^2
+ *   loss [1] = mean over the pairs, rewards [2P] = beta S_i
+ * (Rafailov et al. 2023; label smoothing: Mitchell 2023; margin: Meng et al.
+ * 2024; hinge: Zhao et al. 2023; IPO: Azar et al. 2024.)  ref_logp is read
+ * only where there is a target.  beta > 0, 0 <= label_smoothing <= 1;
+ * label_smoothing must be 0 except for SIGMOID and margin 0 for IPO. */
+#define QLORA_PREF_SIGMOID 0
+#define QLORA_PREF_HINGE 1
+#define QLORA_PREF_IPO 2
+QLORA_API int preference_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float logit_scale,
+                              const int64_t* targets, const int32_t* cu_seqlens, int64_t P, const float* ref_logp,
+                              int kind, float beta, float label_smoothing, float margin, int average,
+                              float grad_scale, float* loss, float* rewards, float* logp, void* dlogits, int64_t ldd,
+                              void* ws, size_t ws_bytes, qlora_stream_t stream);
+
+/* Clipped policy loss with a KL term (Schulman et al. 2017; the KL estimator
+ * of Schulman 2020, the per-token form of Shao et al. 2024).  Per row with a
+ * target and weights[m] != 0, the other rows (their advantage, old_logp and
+ * ref_logp are not used) giving logp 0 and gradient 0:
+ *   rho  = exp(logp - old_logp)    (old_logp NULL: 1, with the same gradient)
+ *   pol  = -min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A)
+ *   kl   = exp(d) - d - 1, d = ref_logp - logp    (ref_logp NULL: 0)
+ *   loss = sum of weights (pol + kl_coef kl)
+ *   stats [4] = loss, sum w pol, sum w kl, sum of w over the clipped rows
+ * The gradient of pol is zero where the clipped term is the strictly smaller
+ * one and -rho A elsewhere.  The weights carry the mask and the normalisation
+ * (1 / number of tokens, 1 / (sequences * length), ...).
+ * 0 <= clip_low <= 1, clip_high >= 0 and finite. */
+QLORA_API int policy_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float logit_scale,
+                          const int64_t* targets, const float* advantages, const float* weights,
+                          const float* old_logp, const float* ref_logp, float clip_low, float clip_high,
+                          float kl_coef, float grad_scale, float* stats, float* logp, void* dlogits, int64_t ldd,
+                          void* ws, size_t ws_bytes, qlora_stream_t stream);
+
 /* Human-readable text for a status code (static storage). */
 QLORA_API const char* qlora_status_string(int status);
 
