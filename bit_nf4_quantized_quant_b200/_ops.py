@@ -125,9 +125,10 @@ def _ptr(t):
 
 
 def _stream(stream=None):
+    # the raw handle of the current stream, without the Stream object around it (3.4 -> 0.3 us a call)
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _bits(t: torch.Tensor) -> torch.Tensor:
@@ -352,17 +353,17 @@ def qlora_linear_bwd_dropout(X, dY, w: NF4Weight, A, B, scaling: float, dropout_
 # --------------------------------------------------------------------------
 def _need(t, name: str, dtype, *shape):
     """t is a dense tensor of this type and shape on the current device (the pointers go to the kernels as they are)."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != shape:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape:
         got = f"{t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
         raise ValueError(f"{name}: {dtype} {shape} wanted, got {got}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
     _on_device(t, name)
-    return t
+    return t.data_ptr()
 
 
 def _on_device(t, name: str):
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
 
 
@@ -372,6 +373,10 @@ def _keep(stream, *tensors):
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
+
+
+def _opt(t, name: str, dtype, *shape):
+    return None if t is None else _need(t, name, dtype, *shape)
 
 
 @dataclass
@@ -384,9 +389,9 @@ class Act8Tensor:
     fmt: int = QLORA_ACT8_INT8
 
     def c_struct(self) -> _Act8:
-        _need(self.codes, "codes", torch.uint8, self.M, self.K)
-        _need(self.scales, "scales", torch.uint8, self.M, self.K // QLORA_ACT8_BLOCK)
-        return _Act8(self.codes.data_ptr(), self.scales.data_ptr(), self.M, self.K, self.fmt)
+        return _Act8(_need(self.codes, "codes", torch.uint8, self.M, self.K),
+                     _need(self.scales, "scales", torch.uint8, self.M, self.K // QLORA_ACT8_BLOCK), self.M, self.K,
+                     self.fmt)
 
     @staticmethod
     def empty(M: int, K: int, device="cuda", fmt: int = QLORA_ACT8_INT8) -> "Act8Tensor":
@@ -406,26 +411,30 @@ def act8_quantize(X: torch.Tensor, fmt: int = QLORA_ACT8_INT8, out: Act8Tensor |
                   stream=None) -> Act8Tensor:
     """bf16 X [M, K] (device) -> 8-bit checkpoint."""
     M, K = X.shape
-    _need(X, "X", torch.bfloat16, M, K)
+    px, u8 = _need(X, "X", torch.bfloat16, M, K), torch.uint8
     if out is None:
-        out = Act8Tensor.empty(M, K, X.device, fmt)
+        out = Act8Tensor(X.new_empty((M, K), dtype=u8), X.new_empty((M, K // QLORA_ACT8_BLOCK), dtype=u8), M, K,
+                         int(fmt))
         _keep(stream, out.codes, out.scales)
-    elif (out.M, out.K) != (M, K):
-        raise ValueError(f"out: a checkpoint of {(M, K)} wanted, got {(out.M, out.K)}")
-    out.fmt = int(fmt)
-    st = out.c_struct()
-    _check("act8_quantize", lib().act8_quantize(_ptr(X), M, K, int(fmt), st.codes, st.scales, _stream(stream)))
+        codes, scales = out.codes.data_ptr(), out.scales.data_ptr()
+    else:
+        if (out.M, out.K) != (M, K):
+            raise ValueError(f"out: a checkpoint of {(M, K)} wanted, got {(out.M, out.K)}")
+        out.fmt = int(fmt)
+        st = out.c_struct()
+        codes, scales = st.codes, st.scales
+    _check("act8_quantize", lib().act8_quantize(px, M, K, int(fmt), codes, scales, _stream(stream)))
     return out
 
 
 def act8_dequant(x: Act8Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """8-bit checkpoint -> the bf16 tensor it stands for."""
-    if out is None:
-        out = torch.empty((x.M, x.K), dtype=torch.bfloat16, device=x.codes.device)
-        _keep(stream, out)
-    _need(out, "out", torch.bfloat16, x.M, x.K)
     st = x.c_struct()
-    _check("act8_dequant", lib().act8_dequant(ctypes.byref(st), _ptr(out), _stream(stream)))
+    if out is None:
+        out = x.codes.new_empty((x.M, x.K), dtype=torch.bfloat16)
+        _keep(stream, out)
+    po = _need(out, "out", torch.bfloat16, x.M, x.K)
+    _check("act8_dequant", lib().act8_dequant(ctypes.byref(st), po, _stream(stream)))
     return out
 
 
@@ -444,28 +453,22 @@ def qlora_linear_bwd_act8(X: Act8Tensor, dY, w: NF4Weight, A, B, scaling: float,
                           dropout_p: float = 0.0, seed: int = 0, offset: int = 0, ws=None, stream=None):
     """qlora_linear_bwd (dropout_p > 0: qlora_linear_bwd_dropout) from an 8-bit checkpoint of X; (dX, dA, dB)."""
     M, K, N, r, bf = X.M, w.K, w.N, A.shape[0], torch.bfloat16
-    dev = X.codes.device
-    _need(dY, "dY", bf, M, N)
-    _need(A, "A", bf, r, K)
-    _need(B, "B", bf, N, r)
-    if T is not None:
-        _need(T, "T", bf, M, r)
+    sx, st = X.c_struct(), w.c_struct()
+    pdy, pa, pb = _need(dY, "dY", bf, M, N), _need(A, "A", bf, r, K), _need(B, "B", bf, N, r)
+    pt = _opt(T, "T", bf, M, r)
     if dX is None:
-        dX = torch.empty((M, K), dtype=bf, device=dev)
+        dX = dY.new_empty((M, K))
     if dA is None:
-        dA = torch.empty((r, K), dtype=bf, device=dev)
+        dA = dY.new_empty((r, K))
     if dB is None:
-        dB = torch.empty((N, r), dtype=bf, device=dev)
+        dB = dY.new_empty((N, r))
     if ws is None:
-        ws = act8_workspace(M, N, K, r, dropout_p > 0, dev)
+        ws = act8_workspace(M, N, K, r, dropout_p > 0, dY.device)
     _keep(stream, dX, dA, dB, ws)
-    _need(dX, "dX", bf, M, K)
-    _need(dA, "dA", bf, r, K)
-    _need(dB, "dB", bf, N, r)
-    st, sx = w.c_struct(), X.c_struct()
     _check("qlora_linear_bwd_act8", lib().qlora_linear_bwd_act8(
-        ctypes.byref(sx), _ptr(dY), ctypes.byref(st), _ptr(A), _ptr(B), r, float(scaling), float(dropout_p),
-        int(seed), int(offset), _ptr(T), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), _stream(stream)))
+        ctypes.byref(sx), pdy, ctypes.byref(st), pa, pb, r, float(scaling), float(dropout_p), int(seed), int(offset),
+        pt, _need(dX, "dX", bf, M, K), _need(dA, "dA", bf, r, K), _need(dB, "dB", bf, N, r), ws.data_ptr(),
+        ws.numel(), _stream(stream)))
     return dX, dA, dB
 
 
@@ -475,33 +478,30 @@ def qlora_linear_bwd_act8(X: Act8Tensor, dY, w: NF4Weight, A, B, scaling: float,
 _LOGITS = {torch.bfloat16: QLORA_LOGITS_BF16, torch.float32: QLORA_LOGITS_FP32}
 
 
-def _logits_args(logits, targets, name="logits"):
-    """(dtype, M, V, row pitch) of [M, V] logits whose rows are dense."""
-    if logits.dim() != 2 or logits.dtype not in _LOGITS:
-        raise ValueError(f"{name}: bf16 or fp32 [M, V] wanted, got {logits.dtype} {tuple(logits.shape)}")
-    M, V = logits.shape
-    if V > 1 and logits.stride(1) != 1:
+def _rows(t, name: str):
+    """(type, M, V, row pitch) of a [M, V] tensor of logits or their gradient, whose rows are dense."""
+    dt = _LOGITS.get(t.dtype)
+    if dt is None or t.dim() != 2:
+        raise ValueError(f"{name}: bf16 or fp32 [M, V] wanted, got {t.dtype} {tuple(t.shape)}")
+    M, V = t.shape
+    ld, step = t.stride()
+    if step != 1 and V > 1:
         raise ValueError(f"{name}: the elements of a row are not adjacent")
-    ld = logits.stride(0) if M > 1 else max(V, logits.stride(0))
-    _on_device(logits, name)
-    _need(targets, "targets", torch.int64, M)
-    return _LOGITS[logits.dtype], M, V, ld
+    _on_device(t, name)
+    return dt, M, V, ld if M > 1 else max(V, ld)
 
 
-def _grad_args(dlogits, logits, want):
-    """The gradient tensor (made when `want` and none is given), and its row pitch."""
+def _grad_rows(dlogits, logits, want: bool):
+    """The gradient tensor (made when `want` and none is given), its pointer and row pitch."""
     if dlogits is None:
         if not want:
-            return None, logits.shape[1]
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+            return None, None, logits.shape[1]
+        dlogits = logits.new_empty(logits.shape)
+        return dlogits, dlogits.data_ptr(), logits.shape[1]
     if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
         raise ValueError(f"dlogits: {logits.dtype} {tuple(logits.shape)} wanted, got {dlogits.dtype} "
                          f"{tuple(dlogits.shape)}")
-    if dlogits.shape[1] > 1 and dlogits.stride(1) != 1:
-        raise ValueError("dlogits: the elements of a row are not adjacent")
-    _on_device(dlogits, "dlogits")
-    M, V = dlogits.shape
-    return dlogits, dlogits.stride(0) if M > 1 else max(V, dlogits.stride(0))
+    return dlogits, dlogits.data_ptr(), _rows(dlogits, "dlogits")[3]
 
 
 def loss_workspace_bytes(M: int) -> int:
@@ -518,13 +518,13 @@ def loss_workspace(M: int, device="cuda") -> torch.Tensor:
 def token_logprob(logits: torch.Tensor, targets: torch.Tensor, logit_scale: float = 1.0, out=None,
                   stream=None) -> torch.Tensor:
     """fp32 [M]: log-probability of each row's target (0 where the target is outside [0, V))."""
-    dt, M, V, ld = _logits_args(logits, targets)
+    dt, M, V, ld = _rows(logits, "logits")
+    py, f32 = _need(targets, "targets", torch.int64, M), torch.float32
     if out is None:
-        out = torch.empty(M, dtype=torch.float32, device=logits.device)
+        out = logits.new_empty(M, dtype=f32)
         _keep(stream, out)
-    _need(out, "out", torch.float32, M)
-    _check("token_logprob", lib().token_logprob(_ptr(logits), dt, M, V, ld, float(logit_scale), _ptr(targets),
-                                                _ptr(out), _stream(stream)))
+    _check("token_logprob", lib().token_logprob(logits.data_ptr(), dt, M, V, ld, logit_scale, py,
+                                                _need(out, "out", f32, M), _stream(stream)))
     return out
 
 
@@ -544,24 +544,24 @@ def preference_loss(logits, targets, cu_seqlens, ref_logp, beta: float, kind: in
 
     cu_seqlens int32 [2 P + 1]: pair p prefers sequence 2p to sequence 2p + 1.  ref_logp fp32 [M] or None.
     dlogits may be the logits themselves; with want_grad=False and no dlogits, the loss alone."""
-    dt, M, V, ld = _logits_args(logits, targets)
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 3 or cu_seqlens.numel() % 2 != 1:
+    dt, M, V, ld = _rows(logits, "logits")
+    n, f32 = cu_seqlens.numel(), torch.float32
+    if n < 3 or n % 2 != 1:
         raise ValueError(f"cu_seqlens: [2 P + 1] wanted, got {tuple(cu_seqlens.shape)}")
-    _need(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.numel())
-    P = cu_seqlens.numel() // 2
-    if ref_logp is not None:
-        _need(ref_logp, "ref_logp", torch.float32, M)
-    dlogits, ldd = _grad_args(dlogits, logits, want_grad)
-    dev, f32 = logits.device, torch.float32
-    loss, rewards, logp = (torch.empty(s, dtype=f32, device=dev) for s in ((), (2 * P,), (M,)))
+    py, pc = _need(targets, "targets", torch.int64, M), _need(cu_seqlens, "cu_seqlens", torch.int32, n)
+    pr = _opt(ref_logp, "ref_logp", f32, M)
+    dlogits, pd, ldd = _grad_rows(dlogits, logits, want_grad)
+    out = logits.new_empty(M + n, dtype=f32)
+    logp, rewards, loss = out.split((M, n - 1, 1))
     if ws is None:
-        ws = loss_workspace(M, dev)
-    _keep(stream, loss, rewards, logp, dlogits, ws)
+        ws = loss_workspace(M, logits.device)
+    _keep(stream, out, dlogits, ws)
+    po = out.data_ptr()
     _check("preference_loss", lib().preference_loss(
-        _ptr(logits), dt, M, V, ld, float(logit_scale), _ptr(targets), _ptr(cu_seqlens), P, _ptr(ref_logp), int(kind),
-        float(beta), float(label_smoothing), float(margin), int(average), float(grad_scale), _ptr(loss),
-        _ptr(rewards), _ptr(logp), _ptr(dlogits), ldd, _ptr(ws), ws.numel(), _stream(stream)))
-    return PreferenceOut(loss, rewards, logp, dlogits)
+        logits.data_ptr(), dt, M, V, ld, logit_scale, py, pc, n // 2, pr, kind, beta, label_smoothing, margin,
+        bool(average), grad_scale, po + 4 * (M + n - 1), po + 4 * M, po, pd, ldd, ws.data_ptr(), ws.numel(),
+        _stream(stream)))
+    return PreferenceOut(loss.view(()), rewards, logp, dlogits)
 
 
 @dataclass
@@ -578,20 +578,21 @@ def policy_loss(logits, targets, advantages, weights, old_logp, ref_logp, clip_l
 
     advantages, weights fp32 [M]; old_logp, ref_logp fp32 [M] or None (ratio 1, no KL term).
     dlogits may be the logits themselves; with want_grad=False and no dlogits, the loss alone."""
-    dt, M, V, ld = _logits_args(logits, targets)
-    f32, dev = torch.float32, logits.device
-    for t, name in ((advantages, "advantages"), (weights, "weights"), (old_logp, "old_logp"), (ref_logp, "ref_logp")):
-        if t is not None or name in ("advantages", "weights"):
-            _need(t, name, f32, M)
-    dlogits, ldd = _grad_args(dlogits, logits, want_grad)
-    stats, logp = torch.empty(4, dtype=f32, device=dev), torch.empty(M, dtype=f32, device=dev)
+    dt, M, V, ld = _rows(logits, "logits")
+    f32 = torch.float32
+    py = _need(targets, "targets", torch.int64, M)
+    pa, pw = _need(advantages, "advantages", f32, M), _need(weights, "weights", f32, M)
+    po, pr = _opt(old_logp, "old_logp", f32, M), _opt(ref_logp, "ref_logp", f32, M)
+    dlogits, pd, ldd = _grad_rows(dlogits, logits, want_grad)
+    out = logits.new_empty(M + 4, dtype=f32)
+    stats, logp = out.split((4, M))
     if ws is None:
-        ws = loss_workspace(M, dev)
-    _keep(stream, stats, logp, dlogits, ws)
+        ws = loss_workspace(M, logits.device)
+    _keep(stream, out, dlogits, ws)
+    ps = out.data_ptr()
     _check("policy_loss", lib().policy_loss(
-        _ptr(logits), dt, M, V, ld, float(logit_scale), _ptr(targets), _ptr(advantages), _ptr(weights),
-        _ptr(old_logp), _ptr(ref_logp), float(clip_low), float(clip_high), float(kl_coef), float(grad_scale),
-        _ptr(stats), _ptr(logp), _ptr(dlogits), ldd, _ptr(ws), ws.numel(), _stream(stream)))
+        logits.data_ptr(), dt, M, V, ld, logit_scale, py, pa, pw, po, pr, clip_low, clip_high, kl_coef, grad_scale,
+        ps, ps + 16, pd, ldd, ws.data_ptr(), ws.numel(), _stream(stream)))
     return PolicyOut(stats, logp, dlogits)
 
 

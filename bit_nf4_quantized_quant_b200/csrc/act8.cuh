@@ -31,7 +31,10 @@ namespace act8 {
 
 constexpr int kThreads = 256;
 constexpr int kPasses = 4;                        // 16-byte loads in flight per lane
-constexpr int kWarpChunks = 32 * kPasses;         // chunks of 8 values per warp and segment
+constexpr int kWarpChunks = 32 * kPasses;         // chunks of 8 values per warp
+
+// CTAs for n8 chunks (n8 <= 2^37: the most that act8_sizes admits)
+inline unsigned grid_of(int64_t n8) { return (unsigned)cdiv(n8, (int64_t)kWarpChunks * (kThreads / 32)); }
 
 // fp32 value of the scale byte: 2^(b - 127), 2^-127 as a subnormal, 255 -> NaN
 __device__ __forceinline__ float scale_of(uint32_t b) {
@@ -67,50 +70,47 @@ __global__ void __launch_bounds__(kThreads) k_act8_quantize(const uint16_t* __re
                                                             uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales) {
     const int lane = threadIdx.x & 31;
-    const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
-    for (int64_t seg = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; seg * kWarpChunks < n8; seg += nwarps) {
-        const int64_t c0 = seg * kWarpChunks + lane;
-        uint4 x[kPasses];
+    const int64_t c0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kWarpChunks + lane;
+    uint4 x[kPasses];
 #pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-            const int64_t c = c0 + 32 * p;
-            x[p] = c < n8 ? ldg_nc_v4(X + 8 * c) : make_uint4(0, 0, 0, 0);
+    for (int p = 0; p < kPasses; ++p) {
+        const int64_t c = c0 + 32 * p;
+        x[p] = c < n8 ? ldg_nc_v4(X + 8 * c) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+        const int64_t c = c0 + 32 * p;
+        const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
+        uint32_t a = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                              __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+        a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        const int amax = (int)max(a & 0xffffu, a >> 16);
+        const bool bad = amax >= 0x7f80;
+        int sb = E4M3 ? (amax >> 7) - 8 + ((amax & 0x7f) > 0x60 ? 1 : 0) : (amax >> 7) - 6;
+        sb = bad ? 255 : max(sb, 0);
+        // 2^-e = 2^(127 - sb); sb <= 249
+        const float inv = bad ? 0.f : __uint_as_float((uint32_t)(254 - sb) << 23);
+        uint32_t o[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float v0 = bf16lo_to_f32(w[2 * h]), v1 = bf16hi_to_f32(w[2 * h]);
+            const float v2 = bf16lo_to_f32(w[2 * h + 1]), v3 = bf16hi_to_f32(w[2 * h + 1]);
+            if (E4M3) {
+                o[h] = adam::f32x2_to_e4m3(v0 * inv, v1 * inv) | (adam::f32x2_to_e4m3(v2 * inv, v3 * inv) << 16);
+            } else {
+                // v inv + 1.5 2^23 rounds v inv to an integer in the low bits, two's complement
+                constexpr float kM = 12582912.f;
+                auto enc = [&](float v) {
+                    return __float_as_uint(fminf(fmaxf(__fmaf_rn(v, inv, kM), kM - 127.f), kM + 127.f));
+                };
+                o[h] = prmt(prmt(enc(v0), enc(v1), 0x0040u), prmt(enc(v2), enc(v3), 0x0040u), 0x5410u);
+            }
         }
-#pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-            const int64_t c = c0 + 32 * p;
-            const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
-            uint32_t a = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                                  __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-            a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, 1));
-            a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, 2));
-            const int amax = (int)max(a & 0xffffu, a >> 16);
-            const bool bad = amax >= 0x7f80;
-            int sb = E4M3 ? (amax >> 7) - 8 + ((amax & 0x7f) > 0x60 ? 1 : 0) : (amax >> 7) - 6;
-            sb = bad ? 255 : max(sb, 0);
-            // 2^-e = 2^(127 - sb); sb <= 249
-            const float inv = bad ? 0.f : __uint_as_float((uint32_t)(254 - sb) << 23);
-            uint32_t o[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float v0 = bf16lo_to_f32(w[2 * h]), v1 = bf16hi_to_f32(w[2 * h]);
-                const float v2 = bf16lo_to_f32(w[2 * h + 1]), v3 = bf16hi_to_f32(w[2 * h + 1]);
-                if (E4M3) {
-                    o[h] = adam::f32x2_to_e4m3(v0 * inv, v1 * inv) | (adam::f32x2_to_e4m3(v2 * inv, v3 * inv) << 16);
-                } else {
-                    // v inv + 1.5 2^23 rounds v inv to an integer in the low bits, two's complement
-                    constexpr float kM = 12582912.f;
-                    auto enc = [&](float v) {
-                        return __float_as_uint(fminf(fmaxf(__fmaf_rn(v, inv, kM), kM - 127.f), kM + 127.f));
-                    };
-                    o[h] = prmt(prmt(enc(v0), enc(v1), 0x0040u), prmt(enc(v2), enc(v3), 0x0040u), 0x5410u);
-                }
-            }
-            if (bad) o[0] = o[1] = 0u;
-            if (c < n8) {
-                *reinterpret_cast<uint2*>(codes + 8 * c) = make_uint2(o[0], o[1]);
-                if ((lane & 3) == 0) scales[c >> 2] = (uint8_t)sb;
-            }
+        if (bad) o[0] = o[1] = 0u;
+        if (c < n8) {
+            *reinterpret_cast<uint2*>(codes + 8 * c) = make_uint2(o[0], o[1]);
+            if ((lane & 3) == 0) scales[c >> 2] = (uint8_t)sb;
         }
     }
 }
@@ -120,30 +120,27 @@ __global__ void __launch_bounds__(kThreads) k_act8_dequant(const uint8_t* __rest
                                                            const uint8_t* __restrict__ scales, int64_t n8,
                                                            uint16_t* __restrict__ out) {
     const int lane = threadIdx.x & 31;
-    const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
-    for (int64_t seg = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; seg * kWarpChunks < n8; seg += nwarps) {
-        const int64_t c0 = seg * kWarpChunks + lane;
-        uint2 q[kPasses];
-        uint32_t sb[kPasses];
+    const int64_t c0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kWarpChunks + lane;
+    uint2 q[kPasses];
+    uint32_t sb[kPasses];
 #pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-            const int64_t c = c0 + 32 * p;
-            q[p] = make_uint2(0, 0);
-            sb[p] = 0;
-            if (c < n8) {
-                q[p] = __ldg(reinterpret_cast<const uint2*>(codes + 8 * c));
-                sb[p] = __ldg(scales + (c >> 2));
-            }
+    for (int p = 0; p < kPasses; ++p) {
+        const int64_t c = c0 + 32 * p;
+        q[p] = make_uint2(0, 0);
+        sb[p] = 0;
+        if (c < n8) {
+            q[p] = __ldg(reinterpret_cast<const uint2*>(codes + 8 * c));
+            sb[p] = __ldg(scales + (c >> 2));
         }
+    }
 #pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-            const int64_t c = c0 + 32 * p;
-            const float s = scale_of(sb[p]);
-            uint4 o;
-            restore4<E4M3>(q[p].x, s, o.x, o.y);
-            restore4<E4M3>(q[p].y, s, o.z, o.w);
-            if (c < n8) *reinterpret_cast<uint4*>(out + 8 * c) = o;
-        }
+    for (int p = 0; p < kPasses; ++p) {
+        const int64_t c = c0 + 32 * p;
+        const float s = scale_of(sb[p]);
+        uint4 o;
+        restore4<E4M3>(q[p].x, s, o.x, o.y);
+        restore4<E4M3>(q[p].y, s, o.z, o.w);
+        if (c < n8) *reinterpret_cast<uint4*>(out + 8 * c) = o;
     }
 }
 

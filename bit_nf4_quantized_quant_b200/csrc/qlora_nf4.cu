@@ -984,9 +984,9 @@ int check_act8(const act8_tensor* x) {
     return QLORA_OK;
 }
 
-int launch_act8_dequant(const act8_tensor* x, uint16_t* out, int sms, cudaStream_t st) {
+int launch_act8_dequant(const act8_tensor* x, uint16_t* out, cudaStream_t st) {
     const int64_t n8 = x->M * x->K / 8;
-    const int grid = grid_for(n8, act8::kWarpChunks * (act8::kThreads / 32), sms, 8);
+    const unsigned grid = act8::grid_of(n8);
     if (x->fmt == QLORA_ACT8_E4M3)
         act8::k_act8_dequant<true><<<grid, act8::kThreads, 0, st>>>(x->codes, x->scales, n8, out);
     else
@@ -1294,7 +1294,7 @@ static int bwd_impl(const qlora_bf16* X, const act8_tensor* x8, const qlora_bf16
     uint8_t* wsb = static_cast<uint8_t*>(ws);
     if (x8) {
         uint16_t* xr = reinterpret_cast<uint16_t*>(wsb + p.total + (dp ? dropout_bytes(M, K) : 0));
-        rc = launch_act8_dequant(x8, xr, sms, st);
+        rc = launch_act8_dequant(x8, xr, st);
         if (rc != QLORA_OK) return rc;
         X = xr;
     }
@@ -1478,11 +1478,10 @@ int act8_quantize(const qlora_bf16* X, int64_t M, int64_t K, int fmt, uint8_t* c
     int rc = check_act8(&x);
     if (rc != QLORA_OK) return rc;
     if (!aligned16(X)) return QLORA_ERR_ALIGN;
-    int sms = 0;
-    rc = check_device(&sms);
+    rc = check_device(nullptr);
     if (rc != QLORA_OK) return rc;
     const int64_t n8 = M * K / 8;
-    const int grid = grid_for(n8, act8::kWarpChunks * (act8::kThreads / 32), sms, 8);
+    const unsigned grid = act8::grid_of(n8);
     if (fmt == QLORA_ACT8_E4M3)
         act8::k_act8_quantize<true><<<grid, act8::kThreads, 0, (cudaStream_t)stream>>>(X, n8, codes, scales);
     else
@@ -1496,10 +1495,9 @@ int act8_dequant(const act8_tensor* x, qlora_bf16* X_out, qlora_stream_t stream)
     int rc = check_act8(x);
     if (rc != QLORA_OK) return rc;
     if (!aligned16(X_out)) return QLORA_ERR_ALIGN;
-    int sms = 0;
-    rc = check_device(&sms);
+    rc = check_device(nullptr);
     if (rc != QLORA_OK) return rc;
-    return launch_act8_dequant(x, X_out, sms, (cudaStream_t)stream);
+    return launch_act8_dequant(x, X_out, (cudaStream_t)stream);
 }
 
 size_t qlora_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int r, int dropout) {
