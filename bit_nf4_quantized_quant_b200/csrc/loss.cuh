@@ -16,11 +16,12 @@
 // tail.
 #pragma once
 #include "common.cuh"
+#include "tc_gemm.cuh"
 
 namespace qnf4 {
 namespace loss {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -72,14 +73,13 @@ template <> struct El<float> {
 // A row's elements before its first 16-byte boundary, its 16-byte vectors, and the rest.
 template <typename T>
 struct Row {
-    int head, tail;
-    int64_t nv;
-    __device__ __forceinline__ Row(const T* x, int64_t V) {
+    int head, tail, nv;
+    __device__ __forceinline__ Row(const T* x, int V) {
         constexpr int N = El<T>::N;
-        const int h = (int)(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T));
-        head = (int64_t)h < V ? h : (int)V;
+        const int h = (int)((16u - ((uint32_t)reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / (int)sizeof(T);
+        head = h < V ? h : V;
         nv = (V - head) / N;
-        tail = (int)(V - head - nv * N);
+        tail = V - head - nv * N;
     }
 };
 
@@ -179,7 +179,8 @@ __device__ __forceinline__ MS row_total(MS v, float c, RowShared& sh, uint32_t r
 // ---------------------------------------------------------------------------
 struct RowArgs {
     const void* logits;
-    int64_t M, V, ld;
+    int64_t M, ld;
+    int V;
     float tau, c;                // logit scale; logit scale * log2 e
     const int64_t* targets;
     float* logp;                 // [M]
@@ -210,11 +211,11 @@ __global__ void __launch_bounds__(kRowThreads) k_token_logprob(const RowArgs a) 
     const T* x = static_cast<const T*>(a.logits) + row * a.ld;
     const float ly = El<T>::get(x[y]);
     const Row<T> sp(x, a.V);
-    const int64_t per = cdiv(sp.nv, z), v0 = rank * per, v1 = v0 + per < sp.nv ? v0 + per : sp.nv;
+    const int per = (sp.nv + (int)z - 1) / (int)z, v0 = rank * per, v1 = v0 + per < sp.nv ? v0 + per : sp.nv;
     const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
     const int bt = blockDim.x, tid = threadIdx.x;
     MS acc{-INFINITY, 0.f};
-    int64_t i = v0 + tid;
+    int i = v0 + tid;
     for (; i + (kUnroll - 1) * bt < v1; i += kUnroll * bt) {
         uint4 v[kUnroll];
 #pragma unroll
@@ -248,7 +249,8 @@ __global__ void __launch_bounds__(kRowThreads) k_token_logprob(const RowArgs a) 
 // ---------------------------------------------------------------------------
 struct GradArgs {
     const void* logits;
-    int64_t M, V, ld;
+    int64_t M, ld;
+    int V;
     float tau, c;
     const int64_t* targets;
     const float2* stats;         // [M] of k_token_logprob
@@ -326,7 +328,8 @@ struct PairArgs {
     const float* logp;           // [M]
     const float* ref;            // [M], or null (reference-free)
     const int64_t* targets;
-    int64_t M, V, P;
+    int64_t M, P;
+    int V;
     const int32_t* cu;           // [2 P + 1]
     int kind, average;
     float beta, smooth, margin, grad_scale;
@@ -473,12 +476,156 @@ __global__ void __launch_bounds__(kPairThreads) k_preference(const PairArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// rows held in registers, the next one on its way into shared memory
+// ---------------------------------------------------------------------------
+// Sum of 2^(c l) over a set of logits as s 2^k with an integer k, so that
+// t = c l - k is one rounding: c l - k in one fused multiply-add, to which the
+// rest c_lo of c (c + c_lo is tau log2 e to 48 bits) is added.  Logits beyond
+// +-2^100 leave the range that k is clamped to; a row's sum is then 0 or
+// infinite, and the row is done again in the careful form above.
+struct __align__(8) KS {
+    float k, s;
+};
+
+constexpr float kTop = 0x1p100f;
+constexpr uint32_t kBulk = 16384;                // bytes per bulk copy
+// CTAs per SM of the kernels that hold a row in registers: as many as leave a
+// thread its NV vectors and 60 registers more (without spills)
+constexpr int engine_ctas(int nt, int nv) { return 65536 / (nt * (nv <= 4 ? 72 : nv <= 8 ? 96 : nv <= 16 ? 128 : 255)); }
+
+__device__ __forceinline__ float round_k(float m, float c) { return rintf(fminf(fmaxf(m * c, -kTop), kTop)); }
+
+typedef unsigned long long f32x2;                // two fp32 in an aligned register pair
+
+__device__ __forceinline__ f32x2 pk2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void un2(f32x2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The pairs of elements of a 16-byte vector.
+template <typename T> struct Pairs;
+template <> struct Pairs<uint16_t> {
+    static constexpr int N = 4;
+    static constexpr uint32_t kNegInf = 0xff80ff80u;
+    static __device__ __forceinline__ f32x2 get(const uint4& v, int j) {
+        const uint32_t w = j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+        return pk2(bf16lo_to_f32(w), bf16hi_to_f32(w));
+    }
+    static __device__ __forceinline__ float max(const uint4& v) {
+        auto b = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+        const __nv_bfloat162 m = __hmax2(__hmax2(b(v.x), b(v.y)), __hmax2(b(v.z), b(v.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+};
+template <> struct Pairs<float> {
+    static constexpr int N = 2;
+    static constexpr uint32_t kNegInf = 0xff800000u;
+    static __device__ __forceinline__ f32x2 get(const uint4& v, int j) {
+        return j == 0 ? pk2(__uint_as_float(v.x), __uint_as_float(v.y))
+                      : pk2(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
+    static __device__ __forceinline__ float max(const uint4& v) {
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+                     fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+};
+
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float warp_sum_f(float v) {
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// Adds up the lanes' (k, s) pairs.
+__device__ __forceinline__ KS warp_total(KS v) {
+    KS o;
+    o.k = warp_max(v.k);
+    o.s = warp_sum_f(v.s * ex2(v.k - o.k));
+    return o;
+}
+
+struct EngineShared {
+    KS warp[kRowThreads / 32];
+    KS rank[2][kMaxZ];                           // written by the CTAs of the cluster, by row parity
+    RowShared careful;
+    float4 row;                                  // what warp 0 made of the row
+    int tick[2];                                 // the row after the next two, by row parity
+    float edge[16];                              // the row's head and tail elements
+    int issued;                                  // copies started
+    unsigned long long bar;
+    int abort;
+};
+
+// Rank 0's warp 0 leaves the ticket in every CTA of the cluster (to be read
+// behind the next barrier).
+__device__ __forceinline__ void share_tick(EngineShared& sh, uint32_t rank, uint32_t z, int parity, int tick) {
+    if (rank != 0 || threadIdx.x >= 32) return;
+    tick = __shfl_sync(0xffffffffu, tick, 0);
+    if (threadIdx.x < z) {
+        const uint32_t at = smem_u32(&sh.tick[parity]);
+        if (z == 1) asm volatile("st.shared.s32 [%0], %1;" ::"r"(at), "r"(tick) : "memory");
+        else asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(mapa(at, threadIdx.x)), "r"(tick) : "memory");
+    }
+    __syncwarp();
+}
+
+// The row's (k, s) in warp 0 of every CTA of the cluster (the other warps
+// return what they have at once): one block barrier, and one cluster barrier
+// for a row that several CTAs share.
+__device__ __forceinline__ KS engine_total(KS v, EngineShared& sh, uint32_t rank, uint32_t z, int parity, int tick) {
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    v = warp_total(v);
+    if (lane == 0) sh.warp[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x < 32) v = warp_total(lane < nw ? sh.warp[lane] : KS{-kTop, 0.f});
+    share_tick(sh, rank, z, parity, tick);
+    if (z == 1) return v;
+    if (threadIdx.x < z) st_dsmem_f2(mapa(smem_u32(&sh.rank[parity][rank]), threadIdx.x), v.k, v.s);
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (threadIdx.x < 32) v = warp_total(lane < (int)z ? sh.rank[parity][lane] : KS{-kTop, 0.f});
+    return v;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // clipped policy loss with a KL term
 // ---------------------------------------------------------------------------
 struct PolicyArgs {
     const void* logits;
-    int64_t M, V, ld;
-    float tau, c;
+    int64_t M, ld;
+    int V;
+    float tau, c, c_lo;          // c + c_lo = tau log2 e
     const int64_t* targets;
     const float* old_logp;       // [M], or null: the ratio is 1 (its gradient stays)
     const float* ref_logp;       // [M], or null: no KL term
@@ -489,105 +636,308 @@ struct PolicyArgs {
     float4* part;                // [M] weighted (loss, policy, kl, clipped)
     void* out;                   // gradient, or null; may be the logits themselves (ldo == ld)
     int64_t ldo;
+    int* ticket;                 // 0 before the launch; null: the rows are dealt out in turn
 };
+
+// The careful form of one row, read again from memory (rows out of k's range:
+// rare): this CTA's vectors [v0, v1) and, in rank 0, the head and the tail.
+template <typename T>
+__device__ __noinline__ MS careful_total(const T* x, int V, int v0, int v1, float c, EngineShared& sh,
+                                         uint32_t rank, uint32_t z) {
+    const Row<T> sp(x, V);
+    MS ms{-INFINITY, 0.f};
+    for (int e = sp.head + v0 * El<T>::N + threadIdx.x; e < sp.head + v1 * El<T>::N; e += blockDim.x)
+        add1(ms, El<T>::get(x[e]), c);
+    if (rank == 0) {
+        if (threadIdx.x < sp.head) add1(ms, El<T>::get(x[threadIdx.x]), c);
+        if (threadIdx.x < sp.tail) add1(ms, El<T>::get(x[V - 1 - threadIdx.x]), c);
+    }
+    if (z > 1) cluster_arrive();
+    ms = row_total(ms, c, sh.careful, rank, z);
+    __syncthreads();
+    if (z > 1) {                                          // sh.careful may be written again by the next such row
+        cluster_arrive();
+        cluster_wait();
+    }
+    return ms;
+}
+
+// Zeroes this CTA's part of a gradient row: 16-byte stores where the row has
+// them, which need not be the boundaries of the logits' row.
+template <typename T>
+__device__ __forceinline__ void zero_row(T* o, int V, int v0, int v1, uint32_t rank) {
+    const Row<T> sp(o, V);
+    // rank q clears vectors [v0, v1), and the last rank that has any also what is left of them
+    uint4* ov = reinterpret_cast<uint4*>(o + sp.head);
+    const int end = v1 < sp.nv ? v1 : sp.nv;
+    for (int i = v0 + threadIdx.x; i < end; i += blockDim.x) ov[i] = make_uint4(0, 0, 0, 0);
+    if (rank == 0) {
+        if (threadIdx.x < sp.head) o[threadIdx.x] = El<T>::put(0.f);
+        if (threadIdx.x < sp.tail) o[V - 1 - threadIdx.x] = El<T>::put(0.f);
+        // the output row may have one vector more than the input row that was dealt out
+        for (int e = sp.head + sp.nv * El<T>::N - El<T>::N + threadIdx.x; sp.nv > 0 && e < sp.head + sp.nv * El<T>::N;
+             e += blockDim.x)
+            o[e] = El<T>::put(0.f);
+    }
+}
+
+// The gradient of a row element by element: in the careful form, and for a
+// gradient row whose 16-byte boundaries are not the logits' (q = -g / S, and
+// k as in the vector path, whose results these equal bit for bit).
+template <typename T>
+__device__ __noinline__ void scalar_grad(const T* x, T* o, int V, int y, int v0, int v1, float c, bool careful, MS ms,
+                                         float k, float q, float g, uint32_t rank) {
+    const Row<T> sp(x, V);
+    auto put = [&](int e) {
+        const float l = El<T>::get(x[e]);
+        if (careful) {
+            const float p = ex2((l - ref_of(ms.m)) * c) / ms.s;
+            o[e] = El<T>::put(e == y ? g - g * p : -g * p);
+        } else {
+            const float p = ex2(fmaf(l, c, -k));
+            o[e] = El<T>::put(e == y ? fmaf(q, p, g) : q * p);
+        }
+    };
+    for (int e = sp.head + v0 * El<T>::N + threadIdx.x; e < sp.head + v1 * El<T>::N; e += blockDim.x) put(e);
+    if (rank == 0) {
+        if (threadIdx.x < sp.head) put(threadIdx.x);
+        if (threadIdx.x < sp.tail) put(V - 1 - threadIdx.x);
+    }
+}
+
+// The row's loss terms (written by thread 0 of rank 0) and d loss / d logit
+// scale: what multiplies 1[v = y] - p_v.
+__device__ __forceinline__ float policy_row(const PolicyArgs& a, int row, float lp, float A, float w, float old,
+                                            float ref, uint32_t rank) {
+    const float rho = a.old_logp ? expf(lp - old) : 1.f;
+    const float free_ = rho * A, held = fminf(fmaxf(rho, a.lo), a.hi) * A;
+    const bool clipped = held < free_;
+    const float d = a.ref_logp ? ref - lp : 0.f, em = expm1f(d);
+    if (rank == 0 && threadIdx.x == 0) {
+        const float pol = -(clipped ? held : free_), kl = em - d;
+        a.logp[row] = lp;
+        a.part[row] = make_float4(w * (pol + a.kl * kl), w * pol, w * kl, clipped ? w : 0.f);
+    }
+    return w * ((clipped ? 0.f : -free_) - a.kl * em) * a.grad_scale * a.tau;
+}
 
 // A row's gradient depends on that row alone, so each row is read once, held
 // in registers (NV vectors per thread of a cluster of z CTAs), and its
-// gradient written: the 2 M V elements that cannot be done without.
-template <typename T, int NV>
-__global__ void __launch_bounds__(kRowThreads, NV >= 16 ? 1 : 2) k_policy(const PolicyArgs a) {
-    __shared__ RowShared sh;
+// gradient written: the 2 M V elements that cannot be done without.  The
+// grid is what the SMs hold, and a cluster has the bulk copy of its next row
+// in flight while it works on one, so that the loads do not wait for the two
+// passes and the reduction.  With many rows the clusters draw them from a
+// counter, three ahead of the work: dealt out in turn, the second CTA of an
+// SM, whose warps are issued after the first one's, ended a quarter later.
+template <typename T, int NT, int NV>
+__global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const PolicyArgs a) {
+    extern __shared__ __align__(128) uint4 buf[];         // this CTA's part of the next row
+    __shared__ EngineShared sh;
     constexpr int N = El<T>::N;
     const uint32_t rank = cluster_rank(), z = cluster_size();
+    const int tid = threadIdx.x;
+    const uint32_t bar = smem_u32(&sh.bar);
+    volatile int* abort = &sh.abort;
+    const uint4 none = make_uint4(Pairs<T>::kNegInf, Pairs<T>::kNegInf, Pairs<T>::kNegInf, Pairs<T>::kNegInf);
+#pragma unroll
+    for (int u = 0; u < NV; ++u) buf[tid + u * NT] = none;
+    if (tid == 0) {
+        sh.abort = 0;
+        sh.issued = 0;
+        tc::mbar_init(bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc::fence_proxy_async();                              // the copies into buf come after these stores
+    __syncthreads();
     if (z > 1) cluster_arrive();
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t row = blockIdx.x / z;
-    const int bt = blockDim.x, tid = threadIdx.x;
-    const int64_t y = a.targets[row];
-    const float w = a.weight[row];
-    const bool live = y >= 0 && y < a.V && w != 0.f;
-    const T* x = static_cast<const T*>(a.logits) + row * a.ld;
-    T* o = static_cast<T*>(a.out) + row * a.ldo;
-    const Row<T> sp(x, a.V);
-    const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
-    const int64_t per = cdiv(sp.nv, z), v0 = rank * per, v1 = v0 + per < sp.nv ? v0 + per : sp.nv;
-    // the one element of the head or the tail that this thread holds
-    const int64_t e1 = rank != 0 ? -1 : tid < sp.head ? tid
-                     : tid >= 8 && tid < 8 + sp.tail ? a.V - sp.tail + tid - 8 : -1;
+    const T* x0 = static_cast<const T*>(a.logits);
+    T* o0 = static_cast<T*>(a.out);
+    const int zlog = __ffs((int)z) - 1, M = (int)a.M, V = a.V, G = gridDim.x >> zlog;     // z is a power of two
 
-    uint4 v[NV];
-    float x1 = -INFINITY, g = 0.f, r = 0.f, ls2 = 0.f;
-    if (live) {
-        const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
-        const int64_t i0 = v0 + tid;
-#pragma unroll
-        for (int u = 0; u < NV; ++u)
-            if (i0 + u * bt < v1) v[u] = ld_v4(xv + i0 + u * bt);
-        if (e1 >= 0) x1 = El<T>::get(x[e1]);
-        const float ly = El<T>::get(x[y]);
-        MS acc{-INFINITY, 0.f};
-#pragma unroll
-        for (int u = 0; u < NV; ++u)
-            if (i0 + u * bt < v1) {
-                float f[N];
-                El<T>::unpack(v[u], f);
-                add(acc, f, a.c);
-            }
-        if (e1 >= 0) add1(acc, x1, a.c);
-        const MS t = row_total(acc, a.c, sh, rank, z);
-        r = ref_of(t.m);
-        ls2 = log2f(t.s);
-        const float lp = (ly - r) * a.tau - logf(t.s);
-        const float A = a.adv[row];
-        const float rho = a.old_logp ? expf(lp - a.old_logp[row]) : 1.f;
-        const float free_ = rho * A, held = fminf(fmaxf(rho, a.lo), a.hi) * A;
-        const bool clipped = held < free_;
-        const float d = a.ref_logp ? a.ref_logp[row] - lp : 0.f;
-        g = w * ((clipped ? 0.f : -free_) - (a.ref_logp ? a.kl * expm1f(d) : 0.f)) * a.grad_scale * a.tau;
-        if (rank == 0 && tid == 0) {
-            const float pol = -(clipped ? held : free_);
-            const float kl = a.ref_logp ? expm1f(d) - d : 0.f;
-            a.logp[row] = lp;
-            a.part[row] = make_float4(w * (pol + a.kl * kl), w * pol, w * kl, clipped ? w : 0.f);
-        }
-    } else {
-        if (z > 1) cluster_wait();
-        if (rank == 0 && tid == 0) {
-            a.logp[row] = 0.f;
-            a.part[row] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-    }
-    if (a.out == nullptr) return;
-    auto one = [&](float l, int64_t e) {
-        const float p = ex2((l - r) * a.c - ls2);
-        return e == y ? g - g * p : -g * p;
+    int waited = 0, parity = 0;
+    // this CTA's vectors of a row, and their copy into buf (one thread)
+    auto span = [&](const Row<T>& sp, int& v0, int& v1) {
+        const int per = (sp.nv + (int)z - 1) >> zlog;
+        v0 = (int)rank * per;
+        v1 = v0 + per < sp.nv ? v0 + per : sp.nv;
     };
-    const int64_t i0 = v0 + tid;
-    uint4* ov = reinterpret_cast<uint4*>(o + sp.head);
+    auto load = [&](int row) {
+        const T* x = x0 + row * a.ld;
+        const Row<T> sp(x, V);
+        int v0, v1;
+        span(sp, v0, v1);
+        const uint32_t bytes = v1 > v0 ? (uint32_t)(v1 - v0) * 16u : 0u;
+        if (*abort) return;                               // nothing is waited for any more
+        ++sh.issued;
+        tc::mbar_expect_tx(bar, bytes);
+        for (uint32_t b = 0; b < bytes; b += kBulk)
+            bulk_load(smem_u32(buf) + b, reinterpret_cast<const uint8_t*>(x + sp.head + v0 * N) + b,
+                      bytes - b < kBulk ? bytes - b : kBulk, bar);
+    };
+    // the row's target, -1 where it takes no part: loaded two rows ahead, looked at one row ahead
+    int64_t raw_y = -1;
+    float raw_w = 0.f;
+    auto fetch = [&](int row) {
+        raw_y = row < M ? a.targets[row] : -1;
+        raw_w = row < M ? a.weight[row] : 0.f;
+    };
+    auto target = [&] { return raw_y >= 0 && raw_y < V && raw_w != 0.f ? (int)raw_y : -1; };
+
+    // what a row's loss takes, one value a lane: the logit of the target, the advantage, the weight, and the
+    // two log-probabilities; loaded a row ahead like the row itself
+    auto meta = [&](int row, int y) {
+        float m = 0.f;
+        const int lane = tid & 31;
+        if (y >= 0) {
+            if (lane == 0) m = El<T>::get(x0[row * a.ld + y]);
+            const float* p = lane == 1 ? a.adv : lane == 2 ? a.weight : lane == 3 ? a.old_logp
+                           : lane == 4 ? a.ref_logp : nullptr;
+            if (p) m = p[row];
+        }
+        return m;
+    };
+
+    int row = blockIdx.x >> zlog;
+    fetch(row);
+    int y = target();
+    int nrow = row + G, row2 = row + 2 * G, tick;
+    fetch(nrow);
+    float mt = meta(row, y);
+    if (y >= 0 && tid == 0) load(row);
+    if (z > 1) cluster_wait();                            // every CTA of the cluster runs
+    for (; row < M; row = nrow, nrow = row2, row2 = tick) {
+        const int ny = target();
+        fetch(row2);
+        tick = row2 + G;
+        if (a.ticket != nullptr && rank == 0 && tid == 0) tick = 3 * G + atomicAdd(a.ticket, 1);
+        const float nmt = meta(nrow, ny);
+        const bool live = y >= 0, nlive = ny >= 0;
+        const T* x = x0 + row * a.ld;
+        T* o = o0 + row * a.ldo;
+        const Row<T> sp(x, V);
+        const bool same = a.out == nullptr ||
+                          ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
+        int v0, v1;
+        span(sp, v0, v1);
+        const int nv = v1 - v0;                           // none where negative
+        // the one element of the head or the tail that this thread holds
+        const int e1 = rank != 0 ? -1 : tid < sp.head ? tid
+                     : tid >= 8 && tid < 8 + sp.tail ? V - sp.tail + tid - 8 : -1;
+        uint4 v[NV];
+        float x1 = -INFINITY, ly = 0.f, g = 0.f, k = 0.f, q = 0.f;
+        bool careful = false;
+        MS ms{0.f, 1.f};
+        if (live) {
+            if (e1 >= 0) x1 = El<T>::get(x[e1]);
+            // buf behind the copy is -inf: a row's part differs from another one's by fewer than 16 vectors
+            // (its alignment moves one, and dealing them out to the CTAs up to z - 1 more), and each is
+            // read by the one thread that clears it here
+            const int past = nv > 0 ? nv + ((tid - nv) & (NT - 1)) : tid;
+            if (past - nv < 16 && past < NV * NT) buf[past] = none;
+            tc::mbar_wait(bar, waited & 1, abort);
+            ++waited;
 #pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        const int64_t i = i0 + u * bt;
-        if (i < v1) {
-            float f[N];
-            const int64_t e0 = sp.head + i * N;
-            if (g != 0.f) {
-                El<T>::unpack(v[u], f);
-#pragma unroll
-                for (int j = 0; j < N; ++j) f[j] = one(f[j], e0 + j);
-            } else {
-#pragma unroll
-                for (int j = 0; j < N; ++j) f[j] = 0.f;
+            for (int u = 0; u < NV; ++u) v[u] = buf[tid + u * NT];
+            if (nlive) {                                  // once all have read buf, the next row may come
+                if (tid < 32) {
+                    asm volatile("barrier.cta.sync 1, %0;" ::"n"(NT) : "memory");
+                    if (tid == 0) load(nrow);
+                } else {
+                    asm volatile("barrier.cta.arrive 1, %0;" ::"n"(NT) : "memory");
+                }
             }
-            if (same) {
-                ov[i] = El<T>::pack(f);
-            } else {
+            float m = x1;
 #pragma unroll
-                for (int j = 0; j < N; ++j) o[e0 + j] = El<T>::put(f[j]);
+            for (int u = 0; u < NV; ++u) m = fmaxf(m, Pairs<T>::max(v[u]));
+            KS acc;
+            acc.k = round_k(m, a.c);
+            const f32x2 c2 = pk2(a.c, a.c), l2 = pk2(a.c_lo, a.c_lo), k2 = pk2(-acc.k, -acc.k);
+            f32x2 s2 = pk2(0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < NV; ++u)
+#pragma unroll
+                for (int j = 0; j < Pairs<T>::N; ++j) {
+                    const f32x2 p = Pairs<T>::get(v[u], j);
+                    float t0, t1;
+                    un2(fma2(p, l2, fma2(p, c2, k2)), t0, t1);
+                    s2 = add2(s2, pk2(ex2(t0), ex2(t1)));
+                }
+            float sa, sb;
+            un2(s2, sa, sb);
+            acc.s = sa + sb + ex2(fmaf(x1, a.c_lo, fmaf(x1, a.c, -acc.k)));
+            const KS t = engine_total(acc, sh, rank, z, parity, tick);
+            auto row_loss = [&](float lp) {
+                return policy_row(a, row, lp, __shfl_sync(0xffffffffu, mt, 1), __shfl_sync(0xffffffffu, mt, 2),
+                                  __shfl_sync(0xffffffffu, mt, 3), __shfl_sync(0xffffffffu, mt, 4), rank);
+            };
+            ly = __shfl_sync(0xffffffffu, mt, 0);
+            if (tid < 32) {
+                // the loss of the row and its derivative, by one warp: sixteen took most of the issue slots
+                const float lp = (fmaf(ly, a.c_lo, fmaf(ly, a.c, -t.k)) - log2f(t.s)) * kLn2;
+                const bool in_range = t.s > 0.f && t.s < INFINITY;
+                g = in_range ? row_loss(lp) : 0.f;
+                if (tid == 0) sh.row = make_float4(t.k, -g / t.s, g, in_range ? 0.f : 1.f);
+            }
+            __syncthreads();
+            tick = sh.tick[parity];
+            const float4 rv = sh.row;
+            k = rv.x; q = rv.y; g = rv.z;
+            careful = rv.w != 0.f;
+            if (careful) {
+                // out of k's range, NaN, or nothing above -inf
+                ms = careful_total(x, V, v0, v1, a.c, sh, rank, z);
+                g = row_loss((ly - ref_of(ms.m)) * a.tau - logf(ms.s));
+            }
+        } else {
+            if (nlive && tid == 0) load(nrow);
+            share_tick(sh, rank, z, parity, tick);
+            if (z == 1) {
+                __syncthreads();
+            } else {
+                cluster_arrive();
+                cluster_wait();
+            }
+            tick = sh.tick[parity];
+            if (rank == 0 && tid == 0) {
+                a.logp[row] = 0.f;
+                a.part[row] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
+        if (a.out == nullptr) {
+        } else if (g == 0.f) {                            // padding, or a loss that is flat here
+            zero_row(o, V, v0, v1, rank);
+        } else if (careful || !same) {
+            scalar_grad(x, o, V, y, v0, v1, a.c, careful, ms, k, q, g, rank);
+        } else {
+            // gradient: -g p, then g is added at the target by the thread that has just written there
+            const f32x2 c2 = pk2(a.c, a.c), k2 = pk2(-k, -k), q2 = pk2(q, q);
+            uint4* ov = reinterpret_cast<uint4*>(o + sp.head + v0 * N);
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+                // the vector is unpacked again: its elements are not kept from the first pass
+                asm volatile("" : "+r"(v[u].x), "+r"(v[u].y), "+r"(v[u].z), "+r"(v[u].w));
+                float f[N];
+#pragma unroll
+                for (int j = 0; j < Pairs<T>::N; ++j) {
+                    float t0, t1;
+                    un2(fma2(Pairs<T>::get(v[u], j), c2, k2), t0, t1);
+                    un2(mul2(pk2(ex2(t0), ex2(t1)), q2), f[2 * j], f[2 * j + 1]);
+                }
+                if (tid + u * NT < nv) ov[tid + u * NT] = El<T>::pack(f);
+            }
+            if (e1 >= 0) o[e1] = El<T>::put(q * ex2(fmaf(x1, a.c, -k)));
+            const int yv = y - sp.head - v0 * N;          // the target among this CTA's vectors
+            const bool mine = yv >= 0 && yv < nv * N ? ((yv / N) & (NT - 1)) == tid : e1 == y;
+            if (mine) o[y] = El<T>::put(fmaf(q, ex2(fmaf(ly, a.c, -k)), g));
+        }
+        parity ^= 1;
+        y = ny;
+        mt = nmt;
     }
-    if (e1 >= 0) o[e1] = El<T>::put(g != 0.f ? one(x1, e1) : 0.f);
+    // after an expired wait: the copy in flight lands before the CTA leaves
+    if (tid == 0 && *abort && sh.issued > 0) tc::mbar_drain(bar, (sh.issued - 1) & 1);
 }
 
 constexpr int kFinishThreads = 1024;

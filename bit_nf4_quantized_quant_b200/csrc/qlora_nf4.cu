@@ -1008,16 +1008,18 @@ int check_logits(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld
     if (dtype != QLORA_LOGITS_BF16 && dtype != QLORA_LOGITS_FP32) return QLORA_ERR_VALUE;
     if (M <= 0 || V <= 0 || V > QLORA_MAX_VOCAB || ld < V || M > ((int64_t)1 << 24) || ld > ((int64_t)1 << 32))
         return QLORA_ERR_SHAPE;
-    if (!(tau > 0.f) || !std::isfinite(tau) || !std::isfinite(tau * loss::kLog2e)) return QLORA_ERR_VALUE;
+    if (!(tau >= 0x1p-40f && tau <= 0x1p40f)) return QLORA_ERR_VALUE;
     if (!aligned_to(logits, logit_bytes(dtype)) || !aligned_to(targets, 8)) return QLORA_ERR_ALIGN;
     return QLORA_OK;
 }
 
-template <typename... KArgs, typename... Args>
-int launch_rows(void (*kern)(KArgs...), int64_t rows, int z, int threads, cudaStream_t st, Args... args) {
+template <typename KArg>
+int launch_rows(void (*kern)(KArg), int64_t rows, int z, int threads, cudaStream_t st, const KArg& args,
+                int smem = 0) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(rows * z));
     cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1026,7 +1028,7 @@ int launch_rows(void (*kern)(KArgs...), int64_t rows, int z, int threads, cudaSt
     at[1].val.clusterDim.x = (unsigned)z; at[1].val.clusterDim.y = 1; at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = z > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args);
     note_launch();
     return e == cudaSuccess ? QLORA_OK : QLORA_ERR_LAUNCH;
 }
@@ -1036,31 +1038,61 @@ int row_threads(int64_t nv) { return nv <= 128 ? 128 : nv <= 1024 ? 256 : loss::
 int launch_logprob(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float tau, const int64_t* targets,
                    float* logp, float2* stats, int sms, cudaStream_t st) {
     loss::RowArgs a{};
-    a.logits = logits; a.M = M; a.V = V; a.ld = ld; a.tau = tau; a.c = tau * loss::kLog2e;
+    a.logits = logits; a.M = M; a.V = (int)V; a.ld = ld; a.tau = tau; a.c = tau * loss::kLog2e;
     a.targets = targets; a.logp = logp; a.stats = stats;
     const int64_t nv = V * (int64_t)logit_bytes(dtype) / 16;
     const int threads = row_threads(nv);
     // a row is split over a cluster while the rows alone would not fill the SMs
     int z = 1;
     while (z < loss::kMaxZ && M * z * 2 <= 4 * (int64_t)sms && nv >= 2 * z * threads) z *= 2;
-    return dtype == QLORA_LOGITS_FP32 ? launch_rows(loss::k_token_logprob<float>, M, z, threads, st, a)
-                                      : launch_rows(loss::k_token_logprob<uint16_t>, M, z, threads, st, a);
+    return dtype == QLORA_LOGITS_FP32 ? launch_rows<loss::RowArgs>(loss::k_token_logprob<float>, M, z, threads, st, a)
+                                      : launch_rows<loss::RowArgs>(loss::k_token_logprob<uint16_t>, M, z, threads, st, a);
 }
 
+// The fp32 number c below tau log2 e, and the rest of it.  The rest is positive:
+// with another sign, or 0, the kernels' -inf c + -inf c_lo would be a NaN.
+void split_c(float tau, float* c, float* c_lo) {
+    const double full = (double)tau * 1.4426950408889634074;
+    *c = (float)full;
+    if ((double)*c >= full) *c = std::nextafterf(*c, 0.f);
+    *c_lo = (float)(full - (double)*c);
+}
+
+template <typename T, int NT, int NV>
+int launch_policy_nv(loss::PolicyArgs a, int z, int sms, cudaStream_t st) {
+    static std::atomic<int> set[64];
+    constexpr int smem = NV * NT * 16;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QLORA_ERR_DEVICE;
+    if (set[dev].load() == 0) {
+        if (cudaFuncSetAttribute(loss::k_policy<T, NT, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess)
+            return QLORA_ERR_LAUNCH;
+        set[dev].store(1);
+    }
+    const int64_t slots = (int64_t)sms * loss::engine_ctas(NT, NV) / z;
+    // the counter is cleared by an operation of its own, so only where each cluster takes several rows
+    if (a.M <= 4 * slots) a.ticket = nullptr;
+    else if (cudaMemsetAsync(a.ticket, 0, sizeof(int), st) != cudaSuccess) return QLORA_ERR_LAUNCH;
+    return launch_rows<loss::PolicyArgs>(loss::k_policy<T, NT, NV>, a.M < slots ? a.M : slots, z, NT, st, a, smem);
+}
+
+// Threads and vectors per thread: a row is split over a cluster of z CTAs
+// where it does not fit 16 vectors a thread, or while the rows alone would not
+// give every SM two CTAs.
 template <typename T>
 int launch_policy(const loss::PolicyArgs& a, int sms, cudaStream_t st) {
-    const int64_t nv = a.V * (int64_t)sizeof(T) / 16;
-    const int threads = row_threads(nv);
+    const int nv = a.V * (int)sizeof(T) / 16;
+    if (nv <= 128) return launch_policy_nv<T, 128, 1>(a, 1, sms, st);
     int z = 1;
-    while (z < loss::kMaxZ &&
-           (nv > (int64_t)z * threads * 8 || (a.M * z * 2 <= 2 * (int64_t)sms && nv >= 2 * z * threads)))
-        z *= 2;
-    const int64_t per = cdiv(nv, z);
-    if (per <= threads) return launch_rows(loss::k_policy<T, 1>, a.M, z, threads, st, a);
-    if (per <= 2 * threads) return launch_rows(loss::k_policy<T, 2>, a.M, z, threads, st, a);
-    if (per <= 4 * threads) return launch_rows(loss::k_policy<T, 4>, a.M, z, threads, st, a);
-    if (per <= 8 * threads) return launch_rows(loss::k_policy<T, 8>, a.M, z, threads, st, a);
-    return launch_rows(loss::k_policy<T, 16>, a.M, z, threads, st, a);
+    while (z < loss::kMaxZ && (nv > z * 256 * 16 || (a.M * z * 2 <= 2 * (int64_t)sms && nv >= 2 * z * 256))) z *= 2;
+    const int per = (nv + z - 1) / z;
+    if (per <= 256) return launch_policy_nv<T, 256, 1>(a, z, sms, st);
+    if (per <= 512) return launch_policy_nv<T, 256, 2>(a, z, sms, st);
+    if (per <= 1024) return launch_policy_nv<T, 256, 4>(a, z, sms, st);
+    if (per <= 2048) return launch_policy_nv<T, 256, 8>(a, z, sms, st);
+    if (per <= 4096) return launch_policy_nv<T, 256, 16>(a, z, sms, st);
+    return launch_policy_nv<T, 256, 32>(a, z, sms, st);
 }
 
 }  // namespace
@@ -1530,7 +1562,7 @@ int token_logprob(const void* logits, int dtype, int64_t M, int64_t V, int64_t l
     return launch_logprob(logits, dtype, M, V, ld, logit_scale, targets, logp, nullptr, sms, (cudaStream_t)stream);
 }
 
-size_t loss_workspace_bytes(int64_t M) { return M <= 0 || M > ((int64_t)1 << 24) ? 0 : align256((size_t)M * 16); }
+size_t loss_workspace_bytes(int64_t M) { return M <= 0 || M > ((int64_t)1 << 24) ? 0 : align256((size_t)M * 24) + 256; }
 
 int preference_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float logit_scale,
                     const int64_t* targets, const int32_t* cu_seqlens, int64_t P, const float* ref_logp, int kind,
@@ -1565,17 +1597,17 @@ int preference_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t
     rc = launch_logprob(logits, dtype, M, V, ld, logit_scale, targets, logp, stats, sms, st);
     if (rc != QLORA_OK) return rc;
     loss::PairArgs a{};
-    a.logp = logp; a.ref = ref_logp; a.targets = targets; a.M = M; a.V = V; a.P = P; a.cu = cu_seqlens;
+    a.logp = logp; a.ref = ref_logp; a.targets = targets; a.M = M; a.V = (int)V; a.P = P; a.cu = cu_seqlens;
     a.kind = kind; a.average = average != 0; a.beta = beta; a.smooth = label_smoothing; a.margin = margin;
     a.grad_scale = grad_scale; a.loss = loss; a.rewards = rewards; a.dlogp = dlogits ? dlogp : nullptr;
-    rc = launch_rows(loss::k_preference, 1, loss::kPairCtas, loss::kPairThreads, st, a);
+    rc = launch_rows<loss::PairArgs>(loss::k_preference, 1, loss::kPairCtas, loss::kPairThreads, st, a);
     if (rc != QLORA_OK || !dlogits) return rc;
     loss::GradArgs g{};
-    g.logits = logits; g.M = M; g.V = V; g.ld = ld; g.tau = logit_scale; g.c = logit_scale * loss::kLog2e;
+    g.logits = logits; g.M = M; g.V = (int)V; g.ld = ld; g.tau = logit_scale; g.c = logit_scale * loss::kLog2e;
     g.targets = targets; g.stats = stats; g.dlogp = dlogp; g.out = dlogits; g.ldo = ldd; g.chunks = chunks;
     return dtype == QLORA_LOGITS_FP32
-               ? launch_rows(loss::k_dlogits<float>, M * chunks, 1, loss::kGradThreads, st, g)
-               : launch_rows(loss::k_dlogits<uint16_t>, M * chunks, 1, loss::kGradThreads, st, g);
+               ? launch_rows<loss::GradArgs>(loss::k_dlogits<float>, M * chunks, 1, loss::kGradThreads, st, g)
+               : launch_rows<loss::GradArgs>(loss::k_dlogits<uint16_t>, M * chunks, 1, loss::kGradThreads, st, g);
 }
 
 int policy_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float logit_scale,
@@ -1601,10 +1633,12 @@ int policy_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld,
     if (rc != QLORA_OK) return rc;
     cudaStream_t st = (cudaStream_t)stream;
     loss::PolicyArgs a{};
-    a.logits = logits; a.M = M; a.V = V; a.ld = ld; a.tau = logit_scale; a.c = logit_scale * loss::kLog2e;
+    a.logits = logits; a.M = M; a.V = (int)V; a.ld = ld; a.tau = logit_scale;
+    split_c(logit_scale, &a.c, &a.c_lo);
     a.targets = targets; a.old_logp = old_logp; a.ref_logp = ref_logp; a.adv = advantages; a.weight = weights;
     a.lo = 1.f - clip_low; a.hi = 1.f + clip_high; a.kl = kl_coef; a.grad_scale = grad_scale;
     a.logp = logp; a.part = static_cast<float4*>(ws); a.out = dlogits; a.ldo = ldd;
+    a.ticket = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + align256((size_t)M * 24));
     rc = dtype == QLORA_LOGITS_FP32 ? launch_policy<float>(a, sms, st) : launch_policy<uint16_t>(a, sms, st);
     if (rc != QLORA_OK) return rc;
     return launch_pdl(loss::k_policy_finish, dim3(1), dim3(loss::kFinishThreads), 0, st, (const float4*)a.part, M,

@@ -332,7 +332,8 @@ QLORA_API int qlora_linear_bwd_act8(const act8_tensor* X, const qlora_bf16* dY, 
  *     their element only; 1 <= V <= QLORA_MAX_VOCAB, 1 <= M <= 2^24.
  *   - targets [M] int64.  A row whose target is outside [0, V) takes no part:
  *     its logits are not read, its logp is 0, its gradient row is zero.
- *   - logp_m = tau l_y - ln sum_v exp(tau l_v), tau = logit_scale > 0, in fp32.
+ *   - logp_m = tau l_y - ln sum_v exp(tau l_v), tau = logit_scale in
+ *     [2^-40, 2^40] (else QLORA_ERR_VALUE), in fp32.
  *     Logits of -inf have probability 0; a row that holds a NaN or +inf, or
  *     nothing above -inf, gives NaN.
  *   - dlogits [M, V], rows ldd apart, of the logits' type, or NULL for the

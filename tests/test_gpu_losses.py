@@ -301,6 +301,29 @@ def test_policy(M, V, dtype):
     _run_policy(M + V, M, V, dtype)
 
 
+@pytest.mark.parametrize("V", [40, 2100, 9000, 40000])
+def test_policy_every_row_is_taken_once(V):
+    """Row counts around what the GPU holds at once, and dozens of times that: every row's log-probability and
+    gradient row are those of the row alone."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    base, M0 = _make(V, 64, V, "bf16")[2], 64
+    y0 = torch.arange(M0, device="cuda") * 13 % V
+    w0 = torch.rand(M0, device="cuda") + 0.5
+    w0[::9] = 0
+    adv0 = torch.randn(M0, device="cuda")
+    want = ops.policy_loss(base, y0, adv0, w0, None, None)
+    for M in (sms, 2 * sms + 1, 3 * sms - 1, 6 * sms + 5, 9 * sms, 13 * sms + 1):
+        if M * V > 3e8:
+            continue
+        pick = torch.randint(0, M0, (M,), device="cuda")
+        o = ops.policy_loss(base[pick], y0[pick], adv0[pick], w0[pick], None, None)
+        # a row may be split over another number of CTAs than in the small call: sums in another order
+        assert torch.allclose(o.logp, want.logp[pick], rtol=4 * U, atol=E_LP)
+        d = (o.dlogits.float() - want.dlogits[pick].float()).abs()
+        g = (w0 * adv0.abs())[pick][:, None]
+        assert (d <= 2 * HALF["bf16"] * want.dlogits[pick].float().abs() + 1e-4 * g + 1e-30).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("old,ref", [(False, False), (True, False), (False, True)])
 def test_policy_without_old_or_reference(old, ref, dtype):
