@@ -175,307 +175,6 @@ __device__ __forceinline__ MS row_total(MS v, float c, RowShared& sh, uint32_t r
 }
 
 // ---------------------------------------------------------------------------
-// log-probability of the target
-// ---------------------------------------------------------------------------
-struct RowArgs {
-    const void* logits;
-    int64_t M, ld;
-    int V;
-    float tau, c;                // logit scale; logit scale * log2 e
-    const int64_t* targets;
-    float* logp;                 // [M]
-    float2* stats;               // [M] (r, log2 S), or null
-};
-
-constexpr int kUnroll = 4;
-
-// One row per cluster of z CTAs (z = 1 unless there are few rows).
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) k_token_logprob(const RowArgs a) {
-    __shared__ RowShared sh;
-    constexpr int N = El<T>::N;
-    const uint32_t rank = cluster_rank(), z = cluster_size();
-    if (z > 1) cluster_arrive();
-    grid_dep_wait();
-    grid_dep_launch();
-    const int64_t row = blockIdx.x / z;
-    const int64_t y = a.targets[row];
-    if (y < 0 || y >= a.V) {
-        if (rank == 0 && threadIdx.x == 0) {
-            a.logp[row] = 0.f;
-            if (a.stats) a.stats[row] = make_float2(0.f, 0.f);
-        }
-        if (z > 1) cluster_wait();
-        return;
-    }
-    const T* x = static_cast<const T*>(a.logits) + row * a.ld;
-    const float ly = El<T>::get(x[y]);
-    const Row<T> sp(x, a.V);
-    const int per = (sp.nv + (int)z - 1) / (int)z, v0 = rank * per, v1 = v0 + per < sp.nv ? v0 + per : sp.nv;
-    const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
-    const int bt = blockDim.x, tid = threadIdx.x;
-    MS acc{-INFINITY, 0.f};
-    int i = v0 + tid;
-    for (; i + (kUnroll - 1) * bt < v1; i += kUnroll * bt) {
-        uint4 v[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) v[u] = ld_v4(xv + i + u * bt);
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            float f[N];
-            El<T>::unpack(v[u], f);
-            add(acc, f, a.c);
-        }
-    }
-    for (; i < v1; i += bt) {
-        float f[N];
-        El<T>::unpack(ld_v4(xv + i), f);
-        add(acc, f, a.c);
-    }
-    if (rank == 0) {
-        if (tid < sp.head) add1(acc, El<T>::get(x[tid]), a.c);
-        else if (tid >= 8 && tid < 8 + sp.tail) add1(acc, El<T>::get(x[a.V - sp.tail + tid - 8]), a.c);
-    }
-    const MS t = row_total(acc, a.c, sh, rank, z);
-    if (rank == 0 && tid == 0) {
-        const float r = ref_of(t.m);
-        a.logp[row] = (ly - r) * a.tau - logf(t.s);
-        if (a.stats) a.stats[row] = make_float2(r, log2f(t.s));
-    }
-}
-
-// ---------------------------------------------------------------------------
-// gradient of sum_m d_m logp_m with respect to the logits
-// ---------------------------------------------------------------------------
-struct GradArgs {
-    const void* logits;
-    int64_t M, ld;
-    int V;
-    float tau, c;
-    const int64_t* targets;
-    const float2* stats;         // [M] of k_token_logprob
-    const float* dlogp;          // [M] (not read where the target is outside [0, V))
-    void* out;                   // may be the logits themselves (ldo == ld)
-    int64_t ldo;
-    int64_t chunks;              // per row
-};
-
-constexpr int kGradThreads = 256;
-constexpr int kGradVecs = 4;                     // 16-byte vectors per thread
-
-// One chunk of kGradThreads * kGradVecs vectors of a row per CTA, the last
-// rows first: those are what the forward pass has left in L2.
-template <typename T>
-__global__ void __launch_bounds__(kGradThreads) k_dlogits(const GradArgs a) {
-    constexpr int N = El<T>::N;
-    grid_dep_wait();
-    grid_dep_launch();
-    const int64_t row = a.M - 1 - blockIdx.x / a.chunks;
-    const int64_t ch = blockIdx.x % a.chunks;
-    const T* x = static_cast<const T*>(a.logits) + row * a.ld;
-    T* o = static_cast<T*>(a.out) + row * a.ldo;
-    const int64_t y = a.targets[row];
-    const float d = (y >= 0 && y < a.V) ? a.dlogp[row] * a.tau : 0.f;
-    const float2 st = a.stats[row];
-    const int tid = threadIdx.x;
-    const int64_t cv = (int64_t)kGradThreads * kGradVecs;
-    auto one = [&](float l, int64_t v) {
-        const float p = ex2((l - st.x) * a.c - st.y);
-        return v == y ? d - d * p : -d * p;
-    };
-    if (((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) & 15) != 0) {
-        // the two rows cross 16-byte boundaries at different elements
-        const int64_t e1 = (ch + 1) * cv * N < a.V ? (ch + 1) * cv * N : a.V;
-        for (int64_t e = ch * cv * N + tid; e < e1; e += kGradThreads)
-            o[e] = El<T>::put(d == 0.f ? 0.f : one(El<T>::get(x[e]), e));
-        return;
-    }
-    const Row<T> sp(x, a.V);
-    const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
-    uint4* ov = reinterpret_cast<uint4*>(o + sp.head);
-    const int64_t i0 = ch * cv + tid;
-    if (ch == 0) {
-        const int64_t e = tid < sp.head ? tid : tid >= 8 && tid < 8 + sp.tail ? a.V - sp.tail + tid - 8 : -1;
-        if (e >= 0) o[e] = El<T>::put(d == 0.f ? 0.f : one(El<T>::get(x[e]), e));
-    }
-    if (d == 0.f) {                              // padding, or a loss that is flat here: the logits are not read
-#pragma unroll
-        for (int u = 0; u < kGradVecs; ++u)
-            if (i0 + u * kGradThreads < sp.nv) ov[i0 + u * kGradThreads] = make_uint4(0, 0, 0, 0);
-        return;
-    }
-    uint4 v[kGradVecs];
-#pragma unroll
-    for (int u = 0; u < kGradVecs; ++u)
-        v[u] = i0 + u * kGradThreads < sp.nv ? ld_v4(xv + i0 + u * kGradThreads) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int u = 0; u < kGradVecs; ++u) {
-        const int64_t i = i0 + u * kGradThreads;
-        if (i >= sp.nv) break;
-        float f[N];
-        El<T>::unpack(v[u], f);
-        const int64_t e0 = sp.head + i * N;
-#pragma unroll
-        for (int j = 0; j < N; ++j) f[j] = one(f[j], e0 + j);
-        ov[i] = El<T>::pack(f);
-    }
-}
-
-// ---------------------------------------------------------------------------
-// preference loss over pairs of packed sequences
-// ---------------------------------------------------------------------------
-struct PairArgs {
-    const float* logp;           // [M]
-    const float* ref;            // [M], or null (reference-free)
-    const int64_t* targets;
-    int64_t M, P;
-    int V;
-    const int32_t* cu;           // [2 P + 1]
-    int kind, average;
-    float beta, smooth, margin, grad_scale;
-    float* loss;                 // [1]
-    float* rewards;              // [2 P]
-    float* dlogp;                // [M], or null
-};
-
-constexpr int kPairThreads = 1024, kPairCtas = 8;
-constexpr int kPairWarpTokens = 1024;            // longest pair that one warp takes
-
-struct PairShared {
-    double red[kPairThreads / 32][4];
-    double warp_loss[kPairThreads / 32];
-    double rank_loss[kPairCtas];
-    uint32_t is_long[32];
-};
-
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
-}
-
-// One pair by one warp (CTA = false) or by the whole CTA; returns the pair's loss.
-template <bool CTA>
-__device__ __forceinline__ double do_pair(const PairArgs& a, int64_t p, PairShared& sh) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int id = CTA ? threadIdx.x : lane, n = CTA ? kPairThreads : 32;
-    // the boundaries are device data: clamped, so that no value of theirs leads out of the arrays
-    auto at = [&](int64_t i, int64_t lo) {
-        int64_t c = a.cu[i];
-        c = c < lo ? lo : c;
-        return c < a.M ? c : a.M;
-    };
-    const int64_t s0 = at(2 * p, 0), s1 = at(2 * p + 1, s0), s2 = at(2 * p + 2, s1);
-    double t[4] = {0., 0., 0., 0.};              // chosen sum, rejected sum, chosen count, rejected count
-#pragma unroll 4
-    for (int64_t i = s0 + id; i < s2; i += n) {
-        const int64_t y = a.targets[i];
-        const float lp = a.logp[i], rf = a.ref ? a.ref[i] : 0.f;
-        if (y >= 0 && y < a.V) {
-            const double d = (double)lp - (double)rf;
-            if (i < s1) { t[0] += d; t[2] += 1.; }
-            else { t[1] += d; t[3] += 1.; }
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) t[j] = warp_sum(t[j]);
-    if (CTA) {
-        if (lane == 0)
-            for (int j = 0; j < 4; ++j) sh.red[warp][j] = t[j];
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) t[j] = warp_sum(sh.red[lane][j]);
-        __syncthreads();
-    }
-    const double dc = a.average && t[2] > 0. ? 1. / t[2] : 1., dr = a.average && t[3] > 0. ? 1. / t[3] : 1.;
-    const double sc = t[0] * dc, sr = t[1] * dr, delta = sc - sr;
-    const double beta = (double)a.beta, eps = (double)a.smooth;
-    const double zz = beta * delta - (double)a.margin;
-    double l, g;                                 // loss and d loss / d delta
-    if (a.kind == QLORA_PREF_SIGMOID) {
-        const double e = exp(-fabs(zz)), sp = log1p(e);
-        l = (1. - eps) * (sp + fmax(-zz, 0.)) + (eps != 0. ? eps * (sp + fmax(zz, 0.)) : 0.);
-        const double sg = zz >= 0. ? e / (1. + e) : 1. / (1. + e);      // sigmoid(-z)
-        g = beta * (eps * (1. - sg) - (1. - eps) * sg);
-    } else if (a.kind == QLORA_PREF_HINGE) {
-        l = zz < 1. ? 1. - zz : zz == zz ? 0. : zz;
-        g = zz < 1. ? -beta : 0.;
-    } else {
-        const double q = delta - 0.5 / beta;
-        l = q * q;
-        g = 2. * q;
-    }
-    if (id == 0) {
-        a.rewards[2 * p] = (float)(beta * sc);
-        a.rewards[2 * p + 1] = (float)(beta * sr);
-    }
-    if (a.dlogp) {
-        const double k = g * (double)a.grad_scale / (double)a.P;
-        const float gc = (float)(k * dc), gr = (float)(-k * dr);
-        for (int64_t i = s0 + id; i < s2; i += n) a.dlogp[i] = i < s1 ? gc : gr;
-    }
-    return l;
-}
-
-// One cluster.  CTA c owns the pairs c, c + 8, ...: short ones go to its
-// warps, long ones are taken by the whole CTA, so that neither many short nor
-// few long pairs wait on one warp; the assignment and so every sum's order is
-// fixed.  Rows outside every sequence get gradient 0.
-__global__ void __launch_bounds__(kPairThreads) k_preference(const PairArgs a) {
-    __shared__ PairShared sh;
-    const uint32_t rank = cluster_rank();
-    cluster_arrive();
-    grid_dep_wait();
-    grid_dep_launch();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    double acc = 0.;
-    for (int64_t base = 0; base * kPairCtas + rank < a.P; base += kPairThreads) {
-        const int64_t mine = (base + tid) * kPairCtas + rank;
-        bool lng = false;
-        if (mine < a.P) lng = (int64_t)a.cu[2 * mine + 2] - a.cu[2 * mine] > kPairWarpTokens;
-        const uint32_t bits = __ballot_sync(0xffffffffu, lng);
-        if (lane == 0) sh.is_long[warp] = bits;
-        __syncthreads();
-        for (int j = 0; j < 32; ++j) {
-            const int64_t p = (base + 32 * j + warp) * kPairCtas + rank;
-            if (p >= a.P) break;
-            if (!((sh.is_long[j] >> warp) & 1u)) acc += do_pair<false>(a, p, sh);
-        }
-        for (int j = 0; j < 32; ++j)
-            for (uint32_t b = sh.is_long[j]; b; b &= b - 1) {
-                const int64_t p = (base + 32 * j + __ffs(b) - 1) * kPairCtas + rank;
-                const double l = do_pair<true>(a, p, sh);
-                if (warp == 0) acc += l;
-            }
-        __syncthreads();
-    }
-    if (a.dlogp) {
-        int64_t lo = a.cu[0], hi = a.cu[2 * a.P];
-        lo = lo < 0 ? 0 : lo < a.M ? lo : a.M;
-        hi = hi < lo ? lo : hi < a.M ? hi : a.M;
-        for (int64_t i = (int64_t)rank * kPairThreads + tid; i < lo + a.M - hi; i += kPairThreads * kPairCtas)
-            a.dlogp[i < lo ? i : hi + i - lo] = 0.f;
-    }
-    if (lane == 0) sh.warp_loss[warp] = acc;
-    __syncthreads();
-    cluster_wait();
-    if (warp == 0) {
-        const double v = warp_sum(sh.warp_loss[lane]);
-        if (lane == 0)
-            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(mapa(smem_u32(&sh.rank_loss[rank]), 0)), "d"(v)
-                         : "memory");
-    }
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();
-    if (rank == 0 && tid == 0) {
-        double v = 0.;
-        for (int q = 0; q < kPairCtas; ++q) v += sh.rank_loss[q];
-        a.loss[0] = (float)(v / (double)a.P);
-    }
-}
-
-// ---------------------------------------------------------------------------
 // rows held in registers, the next one on its way into shared memory
 // ---------------------------------------------------------------------------
 // Sum of 2^(c l) over a set of logits as s 2^k with an integer k, so that
@@ -618,26 +317,57 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-// ---------------------------------------------------------------------------
-// clipped policy loss with a KL term
-// ---------------------------------------------------------------------------
-struct PolicyArgs {
-    const void* logits;
-    int64_t M, ld;
-    int V;
-    float tau, c, c_lo;          // c + c_lo = tau log2 e
-    const int64_t* targets;
-    const float* old_logp;       // [M], or null: the ratio is 1 (its gradient stays)
-    const float* ref_logp;       // [M], or null: no KL term
-    const float* adv;            // [M]
-    const float* weight;         // [M]; 0: the row takes no part
-    float lo, hi, kl, grad_scale;
-    float* logp;                 // [M]
-    float4* part;                // [M] weighted (loss, policy, kl, clipped)
-    void* out;                   // gradient, or null; may be the logits themselves (ldo == ld)
-    int64_t ldo;
-    int* ticket;                 // 0 before the launch; null: the rows are dealt out in turn
-};
+// One CTA's part of a row: the sum of its exponentials, and its gradient.
+template <typename T, int NV>
+__device__ __forceinline__ KS sum_pass(const uint4 (&v)[NV], float x1, float c, float c_lo) {
+    float m = x1;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) m = fmaxf(m, Pairs<T>::max(v[u]));
+    KS acc;
+    acc.k = round_k(m, c);
+    const f32x2 c2 = pk2(c, c), l2 = pk2(c_lo, c_lo), k2 = pk2(-acc.k, -acc.k);
+    f32x2 s2 = pk2(0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+        for (int j = 0; j < Pairs<T>::N; ++j) {
+            const f32x2 p = Pairs<T>::get(v[u], j);
+            float t0, t1;
+            un2(fma2(p, l2, fma2(p, c2, k2)), t0, t1);
+            s2 = add2(s2, pk2(ex2(t0), ex2(t1)));
+        }
+    float sa, sb;
+    un2(s2, sa, sb);
+    acc.s = sa + sb + ex2(fmaf(x1, c_lo, fmaf(x1, c, -acc.k)));
+    return acc;
+}
+
+// -g p = q ex2(c l - k); g is added at the target by the thread that has just written there.
+template <typename T, int NT, int NV>
+__device__ __forceinline__ void grad_pass(uint4 (&v)[NV], float x1, float ly, T* o, const Row<T>& sp, int v0, int nv,
+                                          int e1, int y, float c, float k, float q, float g) {
+    constexpr int N = El<T>::N;
+    const int tid = threadIdx.x;
+    const f32x2 c2 = pk2(c, c), k2 = pk2(-k, -k), q2 = pk2(q, q);
+    uint4* ov = reinterpret_cast<uint4*>(o + sp.head + v0 * N);
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        // the vector is unpacked again: its elements are not kept from the first pass
+        asm volatile("" : "+r"(v[u].x), "+r"(v[u].y), "+r"(v[u].z), "+r"(v[u].w));
+        float f[N];
+#pragma unroll
+        for (int j = 0; j < Pairs<T>::N; ++j) {
+            float t0, t1;
+            un2(fma2(Pairs<T>::get(v[u], j), c2, k2), t0, t1);
+            un2(mul2(pk2(ex2(t0), ex2(t1)), q2), f[2 * j], f[2 * j + 1]);
+        }
+        if (tid + u * NT < nv) ov[tid + u * NT] = El<T>::pack(f);
+    }
+    if (e1 >= 0) o[e1] = El<T>::put(q * ex2(fmaf(x1, c, -k)));
+    const int yv = y - sp.head - v0 * N;                  // the target among this CTA's vectors
+    const bool mine = yv >= 0 && yv < nv * N ? ((yv / N) & (NT - 1)) == tid : e1 == y;
+    if (mine) o[y] = El<T>::put(fmaf(q, ex2(fmaf(ly, c, -k)), g));
+}
 
 // The careful form of one row, read again from memory (rows out of k's range:
 // rare): this CTA's vectors [v0, v1) and, in rank 0, the head and the tail.
@@ -704,6 +434,400 @@ __device__ __noinline__ void scalar_grad(const T* x, T* o, int V, int y, int v0,
         if (threadIdx.x < sp.tail) put(V - 1 - threadIdx.x);
     }
 }
+
+// ---------------------------------------------------------------------------
+// log-probability of the target
+// ---------------------------------------------------------------------------
+struct RowArgs {
+    const void* logits;
+    int64_t M, ld;
+    int V;
+    float tau, c, c_lo;          // c + c_lo = tau log2 e
+    const int64_t* targets;
+    float* logp;                 // [M]
+    float2* stats;               // [M] or null: (k, S), or (r, -S) for a row in the careful form
+    double* lpd;                 // [M] the log-probability before its rounding to fp32; null without stats
+};
+
+// The row's log-probability from its sum, in fp64; not above 0, which the
+// rounding of a sum that is one term could make it.
+__device__ __forceinline__ double logp_of(float ly, KS t, float c, float c_lo) {
+    const double lp = (((double)c + (double)c_lo) * (double)ly - (double)t.k - log2((double)t.s)) * 0.69314718055994530942;
+    return lp > 0. ? 0. : lp;
+}
+__device__ __forceinline__ double logp_of(float ly, MS t, float tau) {
+    const double lp = ((double)ly - (double)ref_of(t.m)) * (double)tau - log((double)t.s);
+    return lp > 0. ? 0. : lp;
+}
+
+__device__ __forceinline__ bool in_range(float S) { return S > 0.f && S < INFINITY; }
+
+constexpr int kUnroll = 4;
+constexpr float kSlack = 32.f;                   // how far a term's exponent may be above the sum's
+
+// One row per cluster of z CTAs (z = 1 unless there are few rows).  A thread's
+// k moves only when a logit comes that is more than 2^kSlack above it.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) k_token_logprob(const RowArgs a) {
+    __shared__ EngineShared sh;
+    const uint32_t rank = cluster_rank(), z = cluster_size();
+    if (z > 1) {
+        cluster_arrive();
+        cluster_wait();                          // every CTA of the cluster runs
+    }
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t row = blockIdx.x / z;
+    const int64_t y = a.targets[row];
+    if (y < 0 || y >= a.V) {
+        if (rank == 0 && threadIdx.x == 0) {
+            a.logp[row] = 0.f;
+            if (a.stats) {
+                a.stats[row] = make_float2(0.f, 1.f);
+                a.lpd[row] = 0.;
+            }
+        }
+        return;
+    }
+    const T* x = static_cast<const T*>(a.logits) + row * a.ld;
+    const float ly = El<T>::get(x[y]);
+    const Row<T> sp(x, a.V);
+    const int per = (sp.nv + (int)z - 1) / (int)z, v0 = rank * per, v1 = v0 + per < sp.nv ? v0 + per : sp.nv;
+    const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
+    const int bt = blockDim.x, tid = threadIdx.x;
+    KS acc{-kTop, 0.f};
+    const f32x2 c2 = pk2(a.c, a.c), l2 = pk2(a.c_lo, a.c_lo);
+    f32x2 s2 = pk2(0.f, 0.f), k2 = pk2(-acc.k, -acc.k);
+    auto add_vec = [&](const uint4* v, int n) {
+        float m = Pairs<T>::max(v[0]);
+        for (int u = 1; u < n; ++u) m = fmaxf(m, Pairs<T>::max(v[u]));
+        if (fmaf(m, a.c, -acc.k) > kSlack) {
+            const float k = round_k(m, a.c), f = ex2(acc.k - k);
+            s2 = mul2(s2, pk2(f, f));
+            acc.k = k;
+            k2 = pk2(-k, -k);
+        }
+        for (int u = 0; u < n; ++u)
+#pragma unroll
+            for (int j = 0; j < Pairs<T>::N; ++j) {
+                const f32x2 p = Pairs<T>::get(v[u], j);
+                float t0, t1;
+                un2(fma2(p, l2, fma2(p, c2, k2)), t0, t1);
+                s2 = add2(s2, pk2(ex2(t0), ex2(t1)));
+            }
+    };
+    int i = v0 + tid;
+    for (; i + (kUnroll - 1) * bt < v1; i += kUnroll * bt) {
+        uint4 v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) v[u] = ld_v4(xv + i + u * bt);
+        add_vec(v, kUnroll);
+    }
+    for (; i < v1; i += bt) {
+        const uint4 v = ld_v4(xv + i);
+        add_vec(&v, 1);
+    }
+    if (rank == 0) {
+        const int e = tid < sp.head ? tid : tid >= 8 && tid < 8 + sp.tail ? a.V - sp.tail + tid - 8 : -1;
+        if (e >= 0) {
+            const float x1 = El<T>::get(x[e]);
+            if (fmaf(x1, a.c, -acc.k) > kSlack) {
+                const float k = round_k(x1, a.c), f = ex2(acc.k - k);
+                s2 = mul2(s2, pk2(f, f));
+                acc.k = k;
+            }
+            s2 = add2(s2, pk2(ex2(fmaf(x1, a.c_lo, fmaf(x1, a.c, -acc.k))), 0.f));
+        }
+    }
+    float sa, sb;
+    un2(s2, sa, sb);
+    acc.s = sa + sb;
+    const KS t = engine_total(acc, sh, rank, z, 0, 0);
+    if (tid == 0) sh.row.x = in_range(t.s) ? 1.f : 0.f;
+    __syncthreads();
+    if (sh.row.x != 0.f) {
+        if (rank == 0 && tid == 0) {
+            const double lp = logp_of(ly, t, a.c, a.c_lo);
+            a.logp[row] = (float)lp;
+            if (a.stats) {
+                a.stats[row] = make_float2(t.k, t.s);
+                a.lpd[row] = lp;
+            }
+        }
+    } else {
+        const MS ms = careful_total(x, a.V, v0, v1, a.c, sh, rank, z);
+        if (rank == 0 && tid == 0) {
+            const double lp = logp_of(ly, ms, a.tau);
+            a.logp[row] = (float)lp;
+            if (a.stats) {
+                a.stats[row] = make_float2(ref_of(ms.m), -ms.s);
+                a.lpd[row] = lp;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// gradient of sum_m d_m logp_m with respect to the logits
+// ---------------------------------------------------------------------------
+struct GradArgs {
+    const void* logits;
+    int64_t M, ld;
+    int V;
+    float tau, c;
+    const int64_t* targets;
+    const float2* stats;         // [M] of k_token_logprob
+    const float* dlogp;          // [M] (not used where the target is outside [0, V))
+    void* out;                   // may be the logits themselves (ldo == ld)
+    int64_t ldo;
+    int chunks;                  // per row
+};
+
+constexpr int kGradThreads = 256;
+constexpr int kGradVecs = 4;                     // 16-byte vectors per thread
+
+// One chunk of kGradThreads * kGradVecs vectors of a row per CTA, the last
+// rows first: those are what the forward pass has left in L2.
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads) k_dlogits(const GradArgs a) {
+    constexpr int N = El<T>::N;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int row_b = blockIdx.x / (unsigned)a.chunks, ch = blockIdx.x - row_b * a.chunks;
+    const int64_t row = a.M - 1 - row_b;
+    const T* x = static_cast<const T*>(a.logits) + row * a.ld;
+    T* o = static_cast<T*>(a.out) + row * a.ldo;
+    const int64_t y64 = a.targets[row];
+    const float dl = a.dlogp[row];
+    const float2 st = a.stats[row];
+    const int y = y64 >= 0 && y64 < a.V ? (int)y64 : -1;
+    const float g = y >= 0 ? dl * a.tau : 0.f;
+    const int tid = threadIdx.x;
+    constexpr int cv = kGradThreads * kGradVecs;
+    const bool careful = !(st.y > 0.f);          // (r, -S)
+    const float q = -g / (careful ? -st.y : st.y);
+    auto one = [&](float l) { return q * ex2(careful ? (l - st.x) * a.c : fmaf(l, a.c, -st.x)); };
+    auto put = [&](int e) {
+        const float f = one(El<T>::get(x[e]));
+        o[e] = El<T>::put(g == 0.f ? 0.f : e == y ? f + g : f);
+    };
+    if ((((uint32_t)reinterpret_cast<uintptr_t>(x) ^ (uint32_t)reinterpret_cast<uintptr_t>(o)) & 15) != 0) {
+        // the two rows cross 16-byte boundaries at different elements
+        const int e1 = (ch + 1) * cv * N < a.V ? (ch + 1) * cv * N : a.V;
+        for (int e = ch * cv * N + tid; e < e1; e += kGradThreads) put(e);
+        return;
+    }
+    const Row<T> sp(x, a.V);
+    const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
+    uint4* ov = reinterpret_cast<uint4*>(o + sp.head);
+    const int i0 = ch * cv + tid;
+    if (ch == 0) {
+        const int e = tid < sp.head ? tid : tid >= 8 && tid < 8 + sp.tail ? a.V - sp.tail + tid - 8 : -1;
+        if (e >= 0) put(e);
+    }
+    if (g == 0.f) {                              // padding, or a loss that is flat here: the vectors are not read
+#pragma unroll
+        for (int u = 0; u < kGradVecs; ++u)
+            if (i0 + u * kGradThreads < sp.nv) ov[i0 + u * kGradThreads] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    uint4 v[kGradVecs];
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u)
+        v[u] = i0 + u * kGradThreads < sp.nv ? ld_v4(xv + i0 + u * kGradThreads) : make_uint4(0, 0, 0, 0);
+    const int yv = y - sp.head;                  // the target among the vectors
+    const int iy = yv >= 0 && yv < sp.nv * N ? yv / N : -1;
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u) {
+        const int i = i0 + u * kGradThreads;
+        float f[N];
+        El<T>::unpack(v[u], f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) f[j] = one(f[j]);
+        if (i == iy) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (j == (yv & (N - 1))) f[j] += g;
+        }
+        if (i < sp.nv) ov[i] = El<T>::pack(f);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// preference loss over pairs of packed sequences
+// ---------------------------------------------------------------------------
+struct PairArgs {
+    const double* lpd;           // [M]
+    const float* ref;            // [M], or null (reference-free)
+    const int64_t* targets;
+    int64_t M, P;
+    int V;
+    const int32_t* cu;           // [2 P + 1]
+    int kind, average;
+    float beta, smooth, margin, grad_scale;
+    float* loss;                 // [1]
+    float* rewards;              // [2 P]
+    float* dlogp;                // [M], or null
+};
+
+constexpr int kPairThreads = 1024, kPairCtas = 8;
+constexpr int kPairWarpTokens = 1024;            // longest pair that one warp takes
+
+struct PairShared {
+    double red[kPairThreads / 32][4];
+    double warp_loss[kPairThreads / 32];
+    double rank_loss[kPairCtas];
+    uint32_t is_long[32];
+};
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// One pair by one warp (CTA = false) or by the whole CTA; returns the pair's loss.
+template <bool CTA>
+__device__ __forceinline__ double do_pair(const PairArgs& a, int64_t p, PairShared& sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int id = CTA ? threadIdx.x : lane, n = CTA ? kPairThreads : 32;
+    // the boundaries are device data: clamped, so that no value of theirs leads out of the arrays
+    auto at = [&](int64_t i, int64_t lo) {
+        int64_t c = a.cu[i];
+        c = c < lo ? lo : c;
+        return c < a.M ? c : a.M;
+    };
+    const int64_t s0 = at(2 * p, 0), s1 = at(2 * p + 1, s0), s2 = at(2 * p + 2, s1);
+    double t[4] = {0., 0., 0., 0.};              // chosen sum, rejected sum, chosen count, rejected count
+#pragma unroll 4
+    for (int64_t i = s0 + id; i < s2; i += n) {
+        const int64_t y = a.targets[i];
+        const double lp = a.lpd[i];
+        const float rf = a.ref ? a.ref[i] : 0.f;
+        if (y >= 0 && y < a.V) {
+            const double d = lp - (double)rf;
+            if (i < s1) { t[0] += d; t[2] += 1.; }
+            else { t[1] += d; t[3] += 1.; }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[j] = warp_sum(t[j]);
+    if (CTA) {
+        if (lane == 0)
+            for (int j = 0; j < 4; ++j) sh.red[warp][j] = t[j];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t[j] = warp_sum(sh.red[lane][j]);
+        __syncthreads();
+    }
+    const double dc = a.average && t[2] > 0. ? 1. / t[2] : 1., dr = a.average && t[3] > 0. ? 1. / t[3] : 1.;
+    const double sc = t[0] * dc, sr = t[1] * dr, delta = sc - sr;
+    const double beta = (double)a.beta, eps = (double)a.smooth;
+    const double zz = beta * delta - (double)a.margin;
+    double l, g;                                 // loss and d loss / d delta
+    if (a.kind == QLORA_PREF_SIGMOID) {
+        const double e = exp(-fabs(zz)), sp = log1p(e);
+        l = (1. - eps) * (sp + fmax(-zz, 0.)) + (eps != 0. ? eps * (sp + fmax(zz, 0.)) : 0.);
+        const double sg = zz >= 0. ? e / (1. + e) : 1. / (1. + e);      // sigmoid(-z)
+        g = beta * (eps * (1. - sg) - (1. - eps) * sg);
+    } else if (a.kind == QLORA_PREF_HINGE) {
+        l = zz < 1. ? 1. - zz : zz == zz ? 0. : zz;
+        g = zz < 1. ? -beta : 0.;
+    } else {
+        const double q = delta - 0.5 / beta;
+        l = q * q;
+        g = 2. * q;
+    }
+    if (id == 0) {
+        a.rewards[2 * p] = (float)(beta * sc);
+        a.rewards[2 * p + 1] = (float)(beta * sr);
+    }
+    if (a.dlogp) {
+        const double k = g * (double)a.grad_scale / (double)a.P;
+        const float gc = (float)(k * dc), gr = (float)(-k * dr);
+        for (int64_t i = s0 + id; i < s2; i += n) a.dlogp[i] = i < s1 ? gc : gr;
+    }
+    return l;
+}
+
+// One cluster.  CTA c owns the pairs c, c + 8, ...: short ones go to its
+// warps, long ones are taken by the whole CTA, so that neither many short nor
+// few long pairs wait on one warp; the assignment and so every sum's order is
+// fixed.  Rows outside every sequence get gradient 0.
+__global__ void __launch_bounds__(kPairThreads) k_preference(const PairArgs a) {
+    __shared__ PairShared sh;
+    const uint32_t rank = cluster_rank();
+    cluster_arrive();
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    double acc = 0.;
+    for (int64_t base = 0; base * kPairCtas + rank < a.P; base += kPairThreads) {
+        const int64_t mine = (base + tid) * kPairCtas + rank;
+        bool lng = false;
+        if (mine < a.P) lng = (int64_t)a.cu[2 * mine + 2] - a.cu[2 * mine] > kPairWarpTokens;
+        const uint32_t bits = __ballot_sync(0xffffffffu, lng);
+        if (lane == 0) sh.is_long[warp] = bits;
+        __syncthreads();
+        for (int j = 0; j < 32; ++j) {
+            const int64_t p = (base + 32 * j + warp) * kPairCtas + rank;
+            if (p >= a.P) break;
+            if (!((sh.is_long[j] >> warp) & 1u)) acc += do_pair<false>(a, p, sh);
+        }
+        for (int j = 0; j < 32; ++j)
+            for (uint32_t b = sh.is_long[j]; b; b &= b - 1) {
+                const int64_t p = (base + 32 * j + __ffs(b) - 1) * kPairCtas + rank;
+                const double l = do_pair<true>(a, p, sh);
+                if (warp == 0) acc += l;
+            }
+        __syncthreads();
+    }
+    if (a.dlogp) {
+        int64_t lo = a.cu[0], hi = a.cu[2 * a.P];
+        lo = lo < 0 ? 0 : lo < a.M ? lo : a.M;
+        hi = hi < lo ? lo : hi < a.M ? hi : a.M;
+        for (int64_t i = (int64_t)rank * kPairThreads + tid; i < lo + a.M - hi; i += kPairThreads * kPairCtas)
+            a.dlogp[i < lo ? i : hi + i - lo] = 0.f;
+    }
+    if (lane == 0) sh.warp_loss[warp] = acc;
+    __syncthreads();
+    cluster_wait();
+    if (warp == 0) {
+        const double v = warp_sum(sh.warp_loss[lane]);
+        if (lane == 0)
+            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(mapa(smem_u32(&sh.rank_loss[rank]), 0)), "d"(v)
+                         : "memory");
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (rank == 0 && tid == 0) {
+        double v = 0.;
+        for (int q = 0; q < kPairCtas; ++q) v += sh.rank_loss[q];
+        a.loss[0] = (float)(v / (double)a.P);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// clipped policy loss with a KL term
+// ---------------------------------------------------------------------------
+struct PolicyArgs {
+    const void* logits;
+    int64_t M, ld;
+    int V;
+    float tau, c, c_lo;          // c + c_lo = tau log2 e
+    const int64_t* targets;
+    const float* old_logp;       // [M], or null: the ratio is 1 (its gradient stays)
+    const float* ref_logp;       // [M], or null: no KL term
+    const float* adv;            // [M]
+    const float* weight;         // [M]; 0: the row takes no part
+    float lo, hi, kl, grad_scale;
+    float* logp;                 // [M]
+    float4* part;                // [M] weighted (loss, policy, kl, clipped)
+    void* out;                   // gradient, or null; may be the logits themselves (ldo == ld)
+    int64_t ldo;
+    int* ticket;                 // 0 before the launch; null: the rows are dealt out in turn
+};
 
 // The row's loss terms (written by thread 0 of rank 0) and d loss / d logit
 // scale: what multiplies 1[v = y] - p_v.
@@ -848,25 +972,7 @@ __global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const Policy
                     asm volatile("barrier.cta.arrive 1, %0;" ::"n"(NT) : "memory");
                 }
             }
-            float m = x1;
-#pragma unroll
-            for (int u = 0; u < NV; ++u) m = fmaxf(m, Pairs<T>::max(v[u]));
-            KS acc;
-            acc.k = round_k(m, a.c);
-            const f32x2 c2 = pk2(a.c, a.c), l2 = pk2(a.c_lo, a.c_lo), k2 = pk2(-acc.k, -acc.k);
-            f32x2 s2 = pk2(0.f, 0.f);
-#pragma unroll
-            for (int u = 0; u < NV; ++u)
-#pragma unroll
-                for (int j = 0; j < Pairs<T>::N; ++j) {
-                    const f32x2 p = Pairs<T>::get(v[u], j);
-                    float t0, t1;
-                    un2(fma2(p, l2, fma2(p, c2, k2)), t0, t1);
-                    s2 = add2(s2, pk2(ex2(t0), ex2(t1)));
-                }
-            float sa, sb;
-            un2(s2, sa, sb);
-            acc.s = sa + sb + ex2(fmaf(x1, a.c_lo, fmaf(x1, a.c, -acc.k)));
+            const KS acc = sum_pass<T, NV>(v, x1, a.c, a.c_lo);
             const KS t = engine_total(acc, sh, rank, z, parity, tick);
             auto row_loss = [&](float lp) {
                 return policy_row(a, row, lp, __shfl_sync(0xffffffffu, mt, 1), __shfl_sync(0xffffffffu, mt, 2),
@@ -876,9 +982,9 @@ __global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const Policy
             if (tid < 32) {
                 // the loss of the row and its derivative, by one warp: sixteen took most of the issue slots
                 const float lp = (fmaf(ly, a.c_lo, fmaf(ly, a.c, -t.k)) - log2f(t.s)) * kLn2;
-                const bool in_range = t.s > 0.f && t.s < INFINITY;
-                g = in_range ? row_loss(lp) : 0.f;
-                if (tid == 0) sh.row = make_float4(t.k, -g / t.s, g, in_range ? 0.f : 1.f);
+                const bool fine = in_range(t.s);
+                g = fine ? row_loss(lp > 0.f ? 0.f : lp) : 0.f;
+                if (tid == 0) sh.row = make_float4(t.k, -g / t.s, g, fine ? 0.f : 1.f);
             }
             __syncthreads();
             tick = sh.tick[parity];
@@ -888,7 +994,7 @@ __global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const Policy
             if (careful) {
                 // out of k's range, NaN, or nothing above -inf
                 ms = careful_total(x, V, v0, v1, a.c, sh, rank, z);
-                g = row_loss((ly - ref_of(ms.m)) * a.tau - logf(ms.s));
+                g = row_loss((float)logp_of(ly, ms, a.tau));
             }
         } else {
             if (nlive && tid == 0) load(nrow);
@@ -911,26 +1017,7 @@ __global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const Policy
         } else if (careful || !same) {
             scalar_grad(x, o, V, y, v0, v1, a.c, careful, ms, k, q, g, rank);
         } else {
-            // gradient: -g p, then g is added at the target by the thread that has just written there
-            const f32x2 c2 = pk2(a.c, a.c), k2 = pk2(-k, -k), q2 = pk2(q, q);
-            uint4* ov = reinterpret_cast<uint4*>(o + sp.head + v0 * N);
-#pragma unroll
-            for (int u = 0; u < NV; ++u) {
-                // the vector is unpacked again: its elements are not kept from the first pass
-                asm volatile("" : "+r"(v[u].x), "+r"(v[u].y), "+r"(v[u].z), "+r"(v[u].w));
-                float f[N];
-#pragma unroll
-                for (int j = 0; j < Pairs<T>::N; ++j) {
-                    float t0, t1;
-                    un2(fma2(Pairs<T>::get(v[u], j), c2, k2), t0, t1);
-                    un2(mul2(pk2(ex2(t0), ex2(t1)), q2), f[2 * j], f[2 * j + 1]);
-                }
-                if (tid + u * NT < nv) ov[tid + u * NT] = El<T>::pack(f);
-            }
-            if (e1 >= 0) o[e1] = El<T>::put(q * ex2(fmaf(x1, a.c, -k)));
-            const int yv = y - sp.head - v0 * N;          // the target among this CTA's vectors
-            const bool mine = yv >= 0 && yv < nv * N ? ((yv / N) & (NT - 1)) == tid : e1 == y;
-            if (mine) o[y] = El<T>::put(fmaf(q, ex2(fmaf(ly, a.c, -k)), g));
+            grad_pass<T, NT, NV>(v, x1, ly, o, sp, v0, nv, e1, y, a.c, k, q, g);
         }
         parity ^= 1;
         y = ny;

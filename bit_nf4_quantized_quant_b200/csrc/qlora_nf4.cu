@@ -1013,6 +1013,15 @@ int check_logits(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld
     return QLORA_OK;
 }
 
+// The fp32 number c below tau log2 e, and the rest of it.  The rest is positive:
+// with another sign, or 0, the kernels' -inf c + -inf c_lo would be a NaN.
+void split_c(float tau, float* c, float* c_lo) {
+    const double full = (double)tau * 1.4426950408889634074;
+    *c = (float)full;
+    if ((double)*c >= full) *c = std::nextafterf(*c, 0.f);
+    *c_lo = (float)(full - (double)*c);
+}
+
 template <typename KArg>
 int launch_rows(void (*kern)(KArg), int64_t rows, int z, int threads, cudaStream_t st, const KArg& args,
                 int smem = 0) {
@@ -1036,10 +1045,11 @@ int launch_rows(void (*kern)(KArg), int64_t rows, int z, int threads, cudaStream
 int row_threads(int64_t nv) { return nv <= 128 ? 128 : nv <= 1024 ? 256 : loss::kRowThreads; }
 
 int launch_logprob(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float tau, const int64_t* targets,
-                   float* logp, float2* stats, int sms, cudaStream_t st) {
+                   float* logp, float2* stats, double* lpd, int sms, cudaStream_t st) {
     loss::RowArgs a{};
-    a.logits = logits; a.M = M; a.V = (int)V; a.ld = ld; a.tau = tau; a.c = tau * loss::kLog2e;
-    a.targets = targets; a.logp = logp; a.stats = stats;
+    a.logits = logits; a.M = M; a.V = (int)V; a.ld = ld; a.tau = tau;
+    split_c(tau, &a.c, &a.c_lo);
+    a.targets = targets; a.logp = logp; a.stats = stats; a.lpd = lpd;
     const int64_t nv = V * (int64_t)logit_bytes(dtype) / 16;
     const int threads = row_threads(nv);
     // a row is split over a cluster while the rows alone would not fill the SMs
@@ -1047,15 +1057,6 @@ int launch_logprob(const void* logits, int dtype, int64_t M, int64_t V, int64_t 
     while (z < loss::kMaxZ && M * z * 2 <= 4 * (int64_t)sms && nv >= 2 * z * threads) z *= 2;
     return dtype == QLORA_LOGITS_FP32 ? launch_rows<loss::RowArgs>(loss::k_token_logprob<float>, M, z, threads, st, a)
                                       : launch_rows<loss::RowArgs>(loss::k_token_logprob<uint16_t>, M, z, threads, st, a);
-}
-
-// The fp32 number c below tau log2 e, and the rest of it.  The rest is positive:
-// with another sign, or 0, the kernels' -inf c + -inf c_lo would be a NaN.
-void split_c(float tau, float* c, float* c_lo) {
-    const double full = (double)tau * 1.4426950408889634074;
-    *c = (float)full;
-    if ((double)*c >= full) *c = std::nextafterf(*c, 0.f);
-    *c_lo = (float)(full - (double)*c);
 }
 
 template <typename T, int NT, int NV>
@@ -1559,7 +1560,7 @@ int token_logprob(const void* logits, int dtype, int64_t M, int64_t V, int64_t l
     int sms = 0;
     rc = check_device(&sms);
     if (rc != QLORA_OK) return rc;
-    return launch_logprob(logits, dtype, M, V, ld, logit_scale, targets, logp, nullptr, sms, (cudaStream_t)stream);
+    return launch_logprob(logits, dtype, M, V, ld, logit_scale, targets, logp, nullptr, nullptr, sms, (cudaStream_t)stream);
 }
 
 size_t loss_workspace_bytes(int64_t M) { return M <= 0 || M > ((int64_t)1 << 24) ? 0 : align256((size_t)M * 24) + 256; }
@@ -1593,18 +1594,21 @@ int preference_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t
     if (rc != QLORA_OK) return rc;
     cudaStream_t st = (cudaStream_t)stream;
     float2* stats = static_cast<float2*>(ws);
-    float* dlogp = reinterpret_cast<float*>(stats + M);
-    rc = launch_logprob(logits, dtype, M, V, ld, logit_scale, targets, logp, stats, sms, st);
+    double* lpd = reinterpret_cast<double*>(stats + M);
+    float* dlogp = reinterpret_cast<float*>(lpd + M);
+    rc = launch_logprob(logits, dtype, M, V, ld, logit_scale, targets, logp, stats, lpd, sms, st);
     if (rc != QLORA_OK) return rc;
     loss::PairArgs a{};
-    a.logp = logp; a.ref = ref_logp; a.targets = targets; a.M = M; a.V = (int)V; a.P = P; a.cu = cu_seqlens;
+    a.lpd = lpd; a.ref = ref_logp; a.targets = targets; a.M = M; a.V = (int)V; a.P = P; a.cu = cu_seqlens;
     a.kind = kind; a.average = average != 0; a.beta = beta; a.smooth = label_smoothing; a.margin = margin;
     a.grad_scale = grad_scale; a.loss = loss; a.rewards = rewards; a.dlogp = dlogits ? dlogp : nullptr;
     rc = launch_rows<loss::PairArgs>(loss::k_preference, 1, loss::kPairCtas, loss::kPairThreads, st, a);
     if (rc != QLORA_OK || !dlogits) return rc;
     loss::GradArgs g{};
-    g.logits = logits; g.M = M; g.V = (int)V; g.ld = ld; g.tau = logit_scale; g.c = logit_scale * loss::kLog2e;
-    g.targets = targets; g.stats = stats; g.dlogp = dlogp; g.out = dlogits; g.ldo = ldd; g.chunks = chunks;
+    g.logits = logits; g.M = M; g.V = (int)V; g.ld = ld; g.tau = logit_scale;
+    float c_lo;
+    split_c(logit_scale, &g.c, &c_lo);
+    g.targets = targets; g.stats = stats; g.dlogp = dlogp; g.out = dlogits; g.ldo = ldd; g.chunks = (int)chunks;
     return dtype == QLORA_LOGITS_FP32
                ? launch_rows<loss::GradArgs>(loss::k_dlogits<float>, M * chunks, 1, loss::kGradThreads, st, g)
                : launch_rows<loss::GradArgs>(loss::k_dlogits<uint16_t>, M * chunks, 1, loss::kGradThreads, st, g);
