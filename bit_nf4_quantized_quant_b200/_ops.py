@@ -9,6 +9,7 @@ loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -351,20 +352,22 @@ def qlora_linear_bwd_dropout(X, dY, w: NF4Weight, A, B, scaling: float, dropout_
 # --------------------------------------------------------------------------
 # 8-bit activation checkpoints
 # --------------------------------------------------------------------------
-def _need(t, name: str, dtype, *shape):
-    """t is a dense tensor of this type and shape on the current device (the pointers go to the kernels as they are)."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape:
+def _need(t, name: str, dtype, shape: tuple, dev=None) -> int:
+    """The address of t, a dense tensor of this type and shape on the current device (`dev`, where known)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
         got = f"{t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
         raise ValueError(f"{name}: {dtype} {shape} wanted, got {got}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
-    _on_device(t, name)
+    if t.get_device() != dev or dev is None:
+        _on_device(t, name)
     return t.data_ptr()
 
 
-def _on_device(t, name: str):
+def _on_device(t, name: str) -> int:
     if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
+    return t.get_device()
 
 
 def _keep(stream, *tensors):
@@ -375,8 +378,8 @@ def _keep(stream, *tensors):
                 t.record_stream(stream)
 
 
-def _opt(t, name: str, dtype, *shape):
-    return None if t is None else _need(t, name, dtype, *shape)
+def _opt(t, name: str, dtype, shape: tuple, dev=None):
+    return None if t is None else _need(t, name, dtype, shape, dev)
 
 
 @dataclass
@@ -389,8 +392,8 @@ class Act8Tensor:
     fmt: int = QLORA_ACT8_INT8
 
     def c_struct(self) -> _Act8:
-        return _Act8(_need(self.codes, "codes", torch.uint8, self.M, self.K),
-                     _need(self.scales, "scales", torch.uint8, self.M, self.K // QLORA_ACT8_BLOCK), self.M, self.K,
+        return _Act8(_need(self.codes, "codes", torch.uint8, (self.M, self.K)),
+                     _need(self.scales, "scales", torch.uint8, (self.M, self.K // QLORA_ACT8_BLOCK)), self.M, self.K,
                      self.fmt)
 
     @staticmethod
@@ -411,7 +414,7 @@ def act8_quantize(X: torch.Tensor, fmt: int = QLORA_ACT8_INT8, out: Act8Tensor |
                   stream=None) -> Act8Tensor:
     """bf16 X [M, K] (device) -> 8-bit checkpoint."""
     M, K = X.shape
-    px, u8 = _need(X, "X", torch.bfloat16, M, K), torch.uint8
+    px, u8 = _need(X, "X", torch.bfloat16, (M, K)), torch.uint8
     if out is None:
         out = Act8Tensor(X.new_empty((M, K), dtype=u8), X.new_empty((M, K // QLORA_ACT8_BLOCK), dtype=u8), M, K,
                          int(fmt))
@@ -433,7 +436,9 @@ def act8_dequant(x: Act8Tensor, out: torch.Tensor | None = None, stream=None) ->
     if out is None:
         out = x.codes.new_empty((x.M, x.K), dtype=torch.bfloat16)
         _keep(stream, out)
-    po = _need(out, "out", torch.bfloat16, x.M, x.K)
+        po = out.data_ptr()
+    else:
+        po = _need(out, "out", torch.bfloat16, (x.M, x.K))
     _check("act8_dequant", lib().act8_dequant(ctypes.byref(st), po, _stream(stream)))
     return out
 
@@ -454,8 +459,9 @@ def qlora_linear_bwd_act8(X: Act8Tensor, dY, w: NF4Weight, A, B, scaling: float,
     """qlora_linear_bwd (dropout_p > 0: qlora_linear_bwd_dropout) from an 8-bit checkpoint of X; (dX, dA, dB)."""
     M, K, N, r, bf = X.M, w.K, w.N, A.shape[0], torch.bfloat16
     sx, st = X.c_struct(), w.c_struct()
-    pdy, pa, pb = _need(dY, "dY", bf, M, N), _need(A, "A", bf, r, K), _need(B, "B", bf, N, r)
-    pt = _opt(T, "T", bf, M, r)
+    dev = X.codes.get_device()
+    pdy, pa, pb = _need(dY, "dY", bf, (M, N), dev), _need(A, "A", bf, (r, K), dev), _need(B, "B", bf, (N, r), dev)
+    pt = _opt(T, "T", bf, (M, r), dev)
     if dX is None:
         dX = dY.new_empty((M, K))
     if dA is None:
@@ -463,12 +469,15 @@ def qlora_linear_bwd_act8(X: Act8Tensor, dY, w: NF4Weight, A, B, scaling: float,
     if dB is None:
         dB = dY.new_empty((N, r))
     if ws is None:
-        ws = act8_workspace(M, N, K, r, dropout_p > 0, dY.device)
+        n = qlora_act8_workspace_bytes(M, N, K, r, dropout_p > 0)
+        if n == 0:
+            raise QLoRAError("qlora_act8_workspace_bytes", -2)
+        ws = dY.new_empty(n, dtype=torch.uint8)
     _keep(stream, dX, dA, dB, ws)
     _check("qlora_linear_bwd_act8", lib().qlora_linear_bwd_act8(
         ctypes.byref(sx), pdy, ctypes.byref(st), pa, pb, r, float(scaling), float(dropout_p), int(seed), int(offset),
-        pt, _need(dX, "dX", bf, M, K), _need(dA, "dA", bf, r, K), _need(dB, "dB", bf, N, r), ws.data_ptr(),
-        ws.numel(), _stream(stream)))
+        pt, _need(dX, "dX", bf, (M, K), dev), _need(dA, "dA", bf, (r, K), dev), _need(dB, "dB", bf, (N, r), dev),
+        ws.data_ptr(), ws.numel(), _stream(stream)))
     return dX, dA, dB
 
 
@@ -479,7 +488,7 @@ _LOGITS = {torch.bfloat16: QLORA_LOGITS_BF16, torch.float32: QLORA_LOGITS_FP32}
 
 
 def _rows(t, name: str):
-    """(type, M, V, row pitch) of a [M, V] tensor of logits or their gradient, whose rows are dense."""
+    """(type, M, V, row pitch, device) of a [M, V] tensor of logits or their gradient, whose rows are dense."""
     dt = _LOGITS.get(t.dtype)
     if dt is None or t.dim() != 2:
         raise ValueError(f"{name}: bf16 or fp32 [M, V] wanted, got {t.dtype} {tuple(t.shape)}")
@@ -487,8 +496,7 @@ def _rows(t, name: str):
     ld, step = t.stride()
     if step != 1 and V > 1:
         raise ValueError(f"{name}: the elements of a row are not adjacent")
-    _on_device(t, name)
-    return dt, M, V, ld if M > 1 else max(V, ld)
+    return dt, M, V, ld if M > 1 else max(V, ld), _on_device(t, name)
 
 
 def _grad_rows(dlogits, logits, want: bool):
@@ -504,6 +512,7 @@ def _grad_rows(dlogits, logits, want: bool):
     return dlogits, dlogits.data_ptr(), _rows(dlogits, "dlogits")[3]
 
 
+@functools.lru_cache(maxsize=64)
 def loss_workspace_bytes(M: int) -> int:
     return int(lib().loss_workspace_bytes(M))
 
@@ -515,16 +524,35 @@ def loss_workspace(M: int, device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _loss_out(logits, M: int, n: int, ws, stream):
+    """n fp32 outputs and, where the caller brings no workspace, one in front of them in the same allocation:
+    (its address, its bytes, outputs, address of the outputs)."""
+    if ws is not None:
+        out = logits.new_empty(n, dtype=torch.float32)
+        _keep(stream, out, ws)
+        return ws.data_ptr(), ws.numel(), out, out.data_ptr()
+    nb = loss_workspace_bytes(M)
+    if nb == 0:
+        raise QLoRAError("loss_workspace_bytes", -2)
+    out = logits.new_empty(nb // 4 + n, dtype=torch.float32)
+    _keep(stream, out)
+    po = out.data_ptr()
+    return po, nb, out[nb // 4:], po + nb
+
+
 def token_logprob(logits: torch.Tensor, targets: torch.Tensor, logit_scale: float = 1.0, out=None,
                   stream=None) -> torch.Tensor:
     """fp32 [M]: log-probability of each row's target (0 where the target is outside [0, V))."""
-    dt, M, V, ld = _rows(logits, "logits")
-    py, f32 = _need(targets, "targets", torch.int64, M), torch.float32
+    dt, M, V, ld, dev = _rows(logits, "logits")
+    py = _need(targets, "targets", torch.int64, (M,), dev)
     if out is None:
-        out = logits.new_empty(M, dtype=f32)
+        out = logits.new_empty(M, dtype=torch.float32)
         _keep(stream, out)
-    _check("token_logprob", lib().token_logprob(logits.data_ptr(), dt, M, V, ld, logit_scale, py,
-                                                _need(out, "out", f32, M), _stream(stream)))
+        po = out.data_ptr()
+    else:
+        po = _need(out, "out", torch.float32, (M,), dev)
+    _check("token_logprob", lib().token_logprob(logits.data_ptr(), dt, M, V, ld, logit_scale, py, po,
+                                                _stream(stream)))
     return out
 
 
@@ -544,23 +572,20 @@ def preference_loss(logits, targets, cu_seqlens, ref_logp, beta: float, kind: in
 
     cu_seqlens int32 [2 P + 1]: pair p prefers sequence 2p to sequence 2p + 1.  ref_logp fp32 [M] or None.
     dlogits may be the logits themselves; with want_grad=False and no dlogits, the loss alone."""
-    dt, M, V, ld = _rows(logits, "logits")
-    n, f32 = cu_seqlens.numel(), torch.float32
+    dt, M, V, ld, dev = _rows(logits, "logits")
+    n = cu_seqlens.numel()
     if n < 3 or n % 2 != 1:
         raise ValueError(f"cu_seqlens: [2 P + 1] wanted, got {tuple(cu_seqlens.shape)}")
-    py, pc = _need(targets, "targets", torch.int64, M), _need(cu_seqlens, "cu_seqlens", torch.int32, n)
-    pr = _opt(ref_logp, "ref_logp", f32, M)
+    py = _need(targets, "targets", torch.int64, (M,), dev)
+    pc = _need(cu_seqlens, "cu_seqlens", torch.int32, (n,), dev)
+    pr = _opt(ref_logp, "ref_logp", torch.float32, (M,), dev)
     dlogits, pd, ldd = _grad_rows(dlogits, logits, want_grad)
-    out = logits.new_empty(M + n, dtype=f32)
+    pw, nw, out, po = _loss_out(logits, M, M + n, ws, stream)
+    _keep(stream, dlogits)
     logp, rewards, loss = out.split((M, n - 1, 1))
-    if ws is None:
-        ws = loss_workspace(M, logits.device)
-    _keep(stream, out, dlogits, ws)
-    po = out.data_ptr()
     _check("preference_loss", lib().preference_loss(
         logits.data_ptr(), dt, M, V, ld, logit_scale, py, pc, n // 2, pr, kind, beta, label_smoothing, margin,
-        bool(average), grad_scale, po + 4 * (M + n - 1), po + 4 * M, po, pd, ldd, ws.data_ptr(), ws.numel(),
-        _stream(stream)))
+        bool(average), grad_scale, po + 4 * (M + n - 1), po + 4 * M, po, pd, ldd, pw, nw, _stream(stream)))
     return PreferenceOut(loss.view(()), rewards, logp, dlogits)
 
 
@@ -578,21 +603,18 @@ def policy_loss(logits, targets, advantages, weights, old_logp, ref_logp, clip_l
 
     advantages, weights fp32 [M]; old_logp, ref_logp fp32 [M] or None (ratio 1, no KL term).
     dlogits may be the logits themselves; with want_grad=False and no dlogits, the loss alone."""
-    dt, M, V, ld = _rows(logits, "logits")
-    f32 = torch.float32
-    py = _need(targets, "targets", torch.int64, M)
-    pa, pw = _need(advantages, "advantages", f32, M), _need(weights, "weights", f32, M)
-    po, pr = _opt(old_logp, "old_logp", f32, M), _opt(ref_logp, "ref_logp", f32, M)
+    dt, M, V, ld, dev = _rows(logits, "logits")
+    f32, m = torch.float32, (M,)
+    py = _need(targets, "targets", torch.int64, m, dev)
+    pa, pw = _need(advantages, "advantages", f32, m, dev), _need(weights, "weights", f32, m, dev)
+    pl, pr = _opt(old_logp, "old_logp", f32, m, dev), _opt(ref_logp, "ref_logp", f32, m, dev)
     dlogits, pd, ldd = _grad_rows(dlogits, logits, want_grad)
-    out = logits.new_empty(M + 4, dtype=f32)
+    ps, ns, out, po = _loss_out(logits, M, M + 4, ws, stream)
+    _keep(stream, dlogits)
     stats, logp = out.split((4, M))
-    if ws is None:
-        ws = loss_workspace(M, logits.device)
-    _keep(stream, out, dlogits, ws)
-    ps = out.data_ptr()
     _check("policy_loss", lib().policy_loss(
-        logits.data_ptr(), dt, M, V, ld, logit_scale, py, pa, pw, po, pr, clip_low, clip_high, kl_coef, grad_scale,
-        ps, ps + 16, pd, ldd, ws.data_ptr(), ws.numel(), _stream(stream)))
+        logits.data_ptr(), dt, M, V, ld, logit_scale, py, pa, pw, pl, pr, clip_low, clip_high, kl_coef, grad_scale,
+        po, po + 16, pd, ldd, ps, ns, _stream(stream)))
     return PolicyOut(stats, logp, dlogits)
 
 

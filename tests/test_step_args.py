@@ -145,7 +145,7 @@ def test_binding_refuses_what_the_pointers_cannot_say(lib):
     l, y, f = torch.zeros((4, 32), dtype=bf), torch.zeros(4, dtype=torch.int64), torch.zeros(4)
     cu = torch.tensor([0, 2, 4], dtype=torch.int32)
     with pytest.raises(ValueError, match="current CUDA device"):
-        ops._need(f, "f", torch.float32, 4)
+        ops._need(f, "f", torch.float32, (4,))
     for bad in (l.half(), l.view(-1), l.t()):
         with pytest.raises(ValueError, match="logits"):
             ops.token_logprob(bad, y)
@@ -158,6 +158,6 @@ def test_binding_refuses_what_the_pointers_cannot_say(lib):
     with pytest.raises(ValueError, match="codes"):
         ops.Act8Tensor(torch.zeros((4, 64), dtype=torch.int8), torch.zeros((4, 2), dtype=torch.uint8), 4, 64).c_struct()
     with pytest.raises(ValueError, match="contiguous"):
-        ops._need(torch.zeros((4, 4)).t(), "t", torch.float32, 4, 4)
+        ops._need(torch.zeros((4, 4)).t(), "t", torch.float32, (4, 4))
     with pytest.raises(ValueError, match="got NoneType"):
-        ops._need(None, "t", torch.float32, 4)
+        ops._need(None, "t", torch.float32, (4,))
