@@ -504,7 +504,7 @@ def _grad_rows(dlogits, logits, want: bool):
     if dlogits is None:
         if not want:
             return None, None, logits.shape[1]
-        dlogits = logits.new_empty(logits.shape)
+        dlogits = torch.empty_like(logits) if logits.is_contiguous() else logits.new_empty(logits.shape)
         return dlogits, dlogits.data_ptr(), logits.shape[1]
     if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
         raise ValueError(f"dlogits: {logits.dtype} {tuple(logits.shape)} wanted, got {dlogits.dtype} "
@@ -525,19 +525,19 @@ def loss_workspace(M: int, device="cuda") -> torch.Tensor:
 
 
 def _loss_out(logits, M: int, n: int, ws, stream):
-    """n fp32 outputs and, where the caller brings no workspace, one in front of them in the same allocation:
-    (its address, its bytes, outputs, address of the outputs)."""
+    """M log-probabilities and n values in fp32 and, where the caller brings no workspace, one in front of them in
+    the same allocation: (address and bytes of the workspace, address of the outputs, the two outputs)."""
     if ws is not None:
-        out = logits.new_empty(n, dtype=torch.float32)
+        out = logits.new_empty(M + n, dtype=torch.float32)
         _keep(stream, out, ws)
-        return ws.data_ptr(), ws.numel(), out, out.data_ptr()
+        return ws.data_ptr(), ws.numel(), out.data_ptr(), *out.split((M, n))
     nb = loss_workspace_bytes(M)
     if nb == 0:
         raise QLoRAError("loss_workspace_bytes", -2)
-    out = logits.new_empty(nb // 4 + n, dtype=torch.float32)
+    out = logits.new_empty(nb // 4 + M + n, dtype=torch.float32)
     _keep(stream, out)
     po = out.data_ptr()
-    return po, nb, out[nb // 4:], po + nb
+    return po, nb, po + nb, *out.split((nb // 4, M, n))[1:]
 
 
 def token_logprob(logits: torch.Tensor, targets: torch.Tensor, logit_scale: float = 1.0, out=None,
@@ -580,13 +580,12 @@ def preference_loss(logits, targets, cu_seqlens, ref_logp, beta: float, kind: in
     pc = _need(cu_seqlens, "cu_seqlens", torch.int32, (n,), dev)
     pr = _opt(ref_logp, "ref_logp", torch.float32, (M,), dev)
     dlogits, pd, ldd = _grad_rows(dlogits, logits, want_grad)
-    pw, nw, out, po = _loss_out(logits, M, M + n, ws, stream)
+    pw, nw, po, logp, out = _loss_out(logits, M, n, ws, stream)
     _keep(stream, dlogits)
-    logp, rewards, loss = out.split((M, n - 1, 1))
     _check("preference_loss", lib().preference_loss(
         logits.data_ptr(), dt, M, V, ld, logit_scale, py, pc, n // 2, pr, kind, beta, label_smoothing, margin,
         bool(average), grad_scale, po + 4 * (M + n - 1), po + 4 * M, po, pd, ldd, pw, nw, _stream(stream)))
-    return PreferenceOut(loss.view(()), rewards, logp, dlogits)
+    return PreferenceOut(out[-1], out[:-1], logp, dlogits)
 
 
 @dataclass
@@ -609,12 +608,11 @@ def policy_loss(logits, targets, advantages, weights, old_logp, ref_logp, clip_l
     pa, pw = _need(advantages, "advantages", f32, m, dev), _need(weights, "weights", f32, m, dev)
     pl, pr = _opt(old_logp, "old_logp", f32, m, dev), _opt(ref_logp, "ref_logp", f32, m, dev)
     dlogits, pd, ldd = _grad_rows(dlogits, logits, want_grad)
-    ps, ns, out, po = _loss_out(logits, M, M + 4, ws, stream)
+    ps, ns, po, logp, stats = _loss_out(logits, M, 4, ws, stream)
     _keep(stream, dlogits)
-    stats, logp = out.split((4, M))
     _check("policy_loss", lib().policy_loss(
         logits.data_ptr(), dt, M, V, ld, logit_scale, py, pa, pw, pl, pr, clip_low, clip_high, kl_coef, grad_scale,
-        po, po + 16, pd, ldd, ps, ns, _stream(stream)))
+        po + 4 * M, po, pd, ldd, ps, ns, _stream(stream)))
     return PolicyOut(stats, logp, dlogits)
 
 

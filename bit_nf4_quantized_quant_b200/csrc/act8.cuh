@@ -21,7 +21,8 @@
 // holds values 8l..8l+7, so loads and stores of every instruction are
 // contiguous across the warp and the block maximum is two shuffles over 4
 // lanes on packed 16-bit integers (the magnitude order of bf16 is the order
-// of its bit patterns).
+// of its bit patterns).  Launched programmatically: a kernel waits for the one
+// before it before it reads anything.
 #pragma once
 #include "common.cuh"
 #include "adamw8.cuh"
@@ -69,6 +70,8 @@ template <bool E4M3>
 __global__ void __launch_bounds__(kThreads) k_act8_quantize(const uint16_t* __restrict__ X, int64_t n8,
                                                             uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales) {
+    grid_dep_wait();
+    grid_dep_launch();
     const int lane = threadIdx.x & 31;
     const int64_t c0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kWarpChunks + lane;
     uint4 x[kPasses];
@@ -119,6 +122,8 @@ template <bool E4M3>
 __global__ void __launch_bounds__(kThreads) k_act8_dequant(const uint8_t* __restrict__ codes,
                                                            const uint8_t* __restrict__ scales, int64_t n8,
                                                            uint16_t* __restrict__ out) {
+    grid_dep_wait();
+    grid_dep_launch();
     const int lane = threadIdx.x & 31;
     const int64_t c0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kWarpChunks + lane;
     uint2 q[kPasses];

@@ -987,12 +987,8 @@ int check_act8(const act8_tensor* x) {
 int launch_act8_dequant(const act8_tensor* x, uint16_t* out, cudaStream_t st) {
     const int64_t n8 = x->M * x->K / 8;
     const unsigned grid = act8::grid_of(n8);
-    if (x->fmt == QLORA_ACT8_E4M3)
-        act8::k_act8_dequant<true><<<grid, act8::kThreads, 0, st>>>(x->codes, x->scales, n8, out);
-    else
-        act8::k_act8_dequant<false><<<grid, act8::kThreads, 0, st>>>(x->codes, x->scales, n8, out);
-    note_launch();
-    return launch_status();
+    return launch_pdl(x->fmt == QLORA_ACT8_E4M3 ? act8::k_act8_dequant<true> : act8::k_act8_dequant<false>,
+                      dim3(grid), dim3(act8::kThreads), 0, st, x->codes, x->scales, n8, out);
 }
 
 // ---------------------------------------------------------------------------
@@ -1515,12 +1511,8 @@ int act8_quantize(const qlora_bf16* X, int64_t M, int64_t K, int fmt, uint8_t* c
     if (rc != QLORA_OK) return rc;
     const int64_t n8 = M * K / 8;
     const unsigned grid = act8::grid_of(n8);
-    if (fmt == QLORA_ACT8_E4M3)
-        act8::k_act8_quantize<true><<<grid, act8::kThreads, 0, (cudaStream_t)stream>>>(X, n8, codes, scales);
-    else
-        act8::k_act8_quantize<false><<<grid, act8::kThreads, 0, (cudaStream_t)stream>>>(X, n8, codes, scales);
-    note_launch();
-    return launch_status();
+    return launch_pdl(fmt == QLORA_ACT8_E4M3 ? act8::k_act8_quantize<true> : act8::k_act8_quantize<false>, dim3(grid),
+                      dim3(act8::kThreads), 0, (cudaStream_t)stream, X, n8, codes, scales);
 }
 
 int act8_dequant(const act8_tensor* x, qlora_bf16* X_out, qlora_stream_t stream) {
