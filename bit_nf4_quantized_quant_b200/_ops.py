@@ -1,4 +1,4 @@
-"""Thin ctypes binding of libqlora_nf4.so (argument marshalling only).
+"""Thin binding of libqlora_nf4.so (argument marshalling only).
 
 Every function has the name of the C entry point it calls (see
 ``include/qlora_nf4.h``) and takes torch tensors for the device buffers, whose
@@ -9,7 +9,6 @@ loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from dataclasses import dataclass
 
@@ -352,22 +351,48 @@ def qlora_linear_bwd_dropout(X, dY, w: NF4Weight, A, B, scaling: float, dropout_
 # --------------------------------------------------------------------------
 # 8-bit activation checkpoints
 # --------------------------------------------------------------------------
-def _need(t, name: str, dtype, shape: tuple, dev=None) -> int:
-    """The address of t, a dense tensor of this type and shape on the current device (`dev`, where known)."""
+def _need(t, name: str, dtype, shape: tuple) -> int:
+    """The address of t, a dense tensor of this type and shape on the current device."""
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
         got = f"{t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
         raise ValueError(f"{name}: {dtype} {shape} wanted, got {got}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
-    if t.get_device() != dev or dev is None:
-        _on_device(t, name)
+    _on_device(t, name)
     return t.data_ptr()
 
 
-def _on_device(t, name: str) -> int:
+def _on_device(t, name: str):
     if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
-    return t.get_device()
+
+
+def _rows(t, name: str):
+    """t is a [M, V] tensor of logits or their gradient, whose rows are dense."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32) or t.dim() != 2:
+        got = f"{t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ValueError(f"{name}: bf16 or fp32 [M, V] wanted, got {got}")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name}: the elements of a row are not adjacent")
+    _on_device(t, name)
+
+
+_step_mod = None
+
+
+def _step():
+    """The extension that marshals the calls below (raises if it has not been built)."""
+    global _step_mod
+    if _step_mod is None:
+        lib()
+        from . import _step as mod
+        mod.bind(QLoRAError, _need, _rows)
+        _step_mod = mod
+    return _step_mod
+
+
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def _keep(stream, *tensors):
@@ -376,10 +401,6 @@ def _keep(stream, *tensors):
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
-
-
-def _opt(t, name: str, dtype, shape: tuple, dev=None):
-    return None if t is None else _need(t, name, dtype, shape, dev)
 
 
 @dataclass
@@ -413,33 +434,21 @@ def act8_sizes(M: int, K: int):
 def act8_quantize(X: torch.Tensor, fmt: int = QLORA_ACT8_INT8, out: Act8Tensor | None = None,
                   stream=None) -> Act8Tensor:
     """bf16 X [M, K] (device) -> 8-bit checkpoint."""
-    M, K = X.shape
-    px, u8 = _need(X, "X", torch.bfloat16, (M, K)), torch.uint8
     if out is None:
-        out = Act8Tensor(X.new_empty((M, K), dtype=u8), X.new_empty((M, K // QLORA_ACT8_BLOCK), dtype=u8), M, K,
-                         int(fmt))
-        _keep(stream, out.codes, out.scales)
-        codes, scales = out.codes.data_ptr(), out.scales.data_ptr()
-    else:
-        if (out.M, out.K) != (M, K):
-            raise ValueError(f"out: a checkpoint of {(M, K)} wanted, got {(out.M, out.K)}")
-        out.fmt = int(fmt)
-        st = out.c_struct()
-        codes, scales = st.codes, st.scales
-    _check("act8_quantize", lib().act8_quantize(px, M, K, int(fmt), codes, scales, _stream(stream)))
+        codes, scales = _step().act8_quantize(X, fmt, None, None, _raw(stream))
+        _keep(stream, codes, scales)
+        return Act8Tensor(codes, scales, *X.shape, int(fmt))
+    if (out.M, out.K) != X.shape:
+        raise ValueError(f"out: a checkpoint of {tuple(X.shape)} wanted, got {(out.M, out.K)}")
+    _step().act8_quantize(X, fmt, out.codes, out.scales, _raw(stream))
+    out.fmt = int(fmt)
     return out
 
 
 def act8_dequant(x: Act8Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """8-bit checkpoint -> the bf16 tensor it stands for."""
-    st = x.c_struct()
-    if out is None:
-        out = x.codes.new_empty((x.M, x.K), dtype=torch.bfloat16)
-        _keep(stream, out)
-        po = out.data_ptr()
-    else:
-        po = _need(out, "out", torch.bfloat16, (x.M, x.K))
-    _check("act8_dequant", lib().act8_dequant(ctypes.byref(st), po, _stream(stream)))
+    out = _step().act8_dequant(x.codes, x.scales, x.M, x.K, x.fmt, out, _raw(stream))
+    _keep(stream, out)
     return out
 
 
@@ -457,62 +466,18 @@ def act8_workspace(M: int, N: int, K: int, r: int, dropout: bool = False, device
 def qlora_linear_bwd_act8(X: Act8Tensor, dY, w: NF4Weight, A, B, scaling: float, T=None, dX=None, dA=None, dB=None,
                           dropout_p: float = 0.0, seed: int = 0, offset: int = 0, ws=None, stream=None):
     """qlora_linear_bwd (dropout_p > 0: qlora_linear_bwd_dropout) from an 8-bit checkpoint of X; (dX, dA, dB)."""
-    M, K, N, r, bf = X.M, w.K, w.N, A.shape[0], torch.bfloat16
-    sx, st = X.c_struct(), w.c_struct()
-    dev = X.codes.get_device()
-    pdy, pa, pb = _need(dY, "dY", bf, (M, N), dev), _need(A, "A", bf, (r, K), dev), _need(B, "B", bf, (N, r), dev)
-    pt = _opt(T, "T", bf, (M, r), dev)
-    if dX is None:
-        dX = dY.new_empty((M, K))
-    if dA is None:
-        dA = dY.new_empty((r, K))
-    if dB is None:
-        dB = dY.new_empty((N, r))
-    if ws is None:
-        n = qlora_act8_workspace_bytes(M, N, K, r, dropout_p > 0)
-        if n == 0:
-            raise QLoRAError("qlora_act8_workspace_bytes", -2)
-        ws = dY.new_empty(n, dtype=torch.uint8)
-    _keep(stream, dX, dA, dB, ws)
-    _check("qlora_linear_bwd_act8", lib().qlora_linear_bwd_act8(
-        ctypes.byref(sx), pdy, ctypes.byref(st), pa, pb, r, float(scaling), float(dropout_p), int(seed), int(offset),
-        pt, _need(dX, "dX", bf, (M, K), dev), _need(dA, "dA", bf, (r, K), dev), _need(dB, "dB", bf, (N, r), dev),
-        ws.data_ptr(), ws.numel(), _stream(stream)))
-    return dX, dA, dB
+    if stream is not None and ws is None:
+        ws = act8_workspace(X.M, w.N, w.K, A.shape[0], dropout_p > 0, X.codes.device)
+    out = _step().qlora_linear_bwd_act8(X.codes, X.scales, X.M, X.K, X.fmt, w.packed, w.codes, w.scale, w.mean, w.N,
+                                        w.K, w.quant_type, dY, A, B, scaling, dropout_p, seed, offset, T, dX, dA, dB,
+                                        ws, _raw(stream))
+    _keep(stream, *out, ws)
+    return out
 
 
 # --------------------------------------------------------------------------
 # losses on logits
 # --------------------------------------------------------------------------
-_LOGITS = {torch.bfloat16: QLORA_LOGITS_BF16, torch.float32: QLORA_LOGITS_FP32}
-
-
-def _rows(t, name: str):
-    """(type, M, V, row pitch, device) of a [M, V] tensor of logits or their gradient, whose rows are dense."""
-    dt = _LOGITS.get(t.dtype)
-    if dt is None or t.dim() != 2:
-        raise ValueError(f"{name}: bf16 or fp32 [M, V] wanted, got {t.dtype} {tuple(t.shape)}")
-    M, V = t.shape
-    ld, step = t.stride()
-    if step != 1 and V > 1:
-        raise ValueError(f"{name}: the elements of a row are not adjacent")
-    return dt, M, V, ld if M > 1 else max(V, ld), _on_device(t, name)
-
-
-def _grad_rows(dlogits, logits, want: bool):
-    """The gradient tensor (made when `want` and none is given), its pointer and row pitch."""
-    if dlogits is None:
-        if not want:
-            return None, None, logits.shape[1]
-        dlogits = torch.empty_like(logits) if logits.is_contiguous() else logits.new_empty(logits.shape)
-        return dlogits, dlogits.data_ptr(), logits.shape[1]
-    if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
-        raise ValueError(f"dlogits: {logits.dtype} {tuple(logits.shape)} wanted, got {dlogits.dtype} "
-                         f"{tuple(dlogits.shape)}")
-    return dlogits, dlogits.data_ptr(), _rows(dlogits, "dlogits")[3]
-
-
-@functools.lru_cache(maxsize=64)
 def loss_workspace_bytes(M: int) -> int:
     return int(lib().loss_workspace_bytes(M))
 
@@ -524,35 +489,11 @@ def loss_workspace(M: int, device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _loss_out(logits, M: int, n: int, ws, stream):
-    """M log-probabilities and n values in fp32 and, where the caller brings no workspace, one in front of them in
-    the same allocation: (address and bytes of the workspace, address of the outputs, the two outputs)."""
-    if ws is not None:
-        out = logits.new_empty(M + n, dtype=torch.float32)
-        _keep(stream, out, ws)
-        return ws.data_ptr(), ws.numel(), out.data_ptr(), *out.split((M, n))
-    nb = loss_workspace_bytes(M)
-    if nb == 0:
-        raise QLoRAError("loss_workspace_bytes", -2)
-    out = logits.new_empty(nb // 4 + M + n, dtype=torch.float32)
-    _keep(stream, out)
-    po = out.data_ptr()
-    return po, nb, po + nb, *out.split((nb // 4, M, n))[1:]
-
-
 def token_logprob(logits: torch.Tensor, targets: torch.Tensor, logit_scale: float = 1.0, out=None,
                   stream=None) -> torch.Tensor:
     """fp32 [M]: log-probability of each row's target (0 where the target is outside [0, V))."""
-    dt, M, V, ld, dev = _rows(logits, "logits")
-    py = _need(targets, "targets", torch.int64, (M,), dev)
-    if out is None:
-        out = logits.new_empty(M, dtype=torch.float32)
-        _keep(stream, out)
-        po = out.data_ptr()
-    else:
-        po = _need(out, "out", torch.float32, (M,), dev)
-    _check("token_logprob", lib().token_logprob(logits.data_ptr(), dt, M, V, ld, logit_scale, py, po,
-                                                _stream(stream)))
+    out = _step().token_logprob(logits, targets, logit_scale, out, _raw(stream))
+    _keep(stream, out)
     return out
 
 
@@ -572,20 +513,12 @@ def preference_loss(logits, targets, cu_seqlens, ref_logp, beta: float, kind: in
 
     cu_seqlens int32 [2 P + 1]: pair p prefers sequence 2p to sequence 2p + 1.  ref_logp fp32 [M] or None.
     dlogits may be the logits themselves; with want_grad=False and no dlogits, the loss alone."""
-    dt, M, V, ld, dev = _rows(logits, "logits")
-    n = cu_seqlens.numel()
-    if n < 3 or n % 2 != 1:
-        raise ValueError(f"cu_seqlens: [2 P + 1] wanted, got {tuple(cu_seqlens.shape)}")
-    py = _need(targets, "targets", torch.int64, (M,), dev)
-    pc = _need(cu_seqlens, "cu_seqlens", torch.int32, (n,), dev)
-    pr = _opt(ref_logp, "ref_logp", torch.float32, (M,), dev)
-    dlogits, pd, ldd = _grad_rows(dlogits, logits, want_grad)
-    pw, nw, po, logp, out = _loss_out(logits, M, n, ws, stream)
-    _keep(stream, dlogits)
-    _check("preference_loss", lib().preference_loss(
-        logits.data_ptr(), dt, M, V, ld, logit_scale, py, pc, n // 2, pr, kind, beta, label_smoothing, margin,
-        bool(average), grad_scale, po + 4 * (M + n - 1), po + 4 * M, po, pd, ldd, pw, nw, _stream(stream)))
-    return PreferenceOut(out[-1], out[:-1], logp, dlogits)
+    if stream is not None and ws is None:
+        ws = loss_workspace(logits.shape[0], logits.device)
+    out = _step().preference_loss(logits, targets, cu_seqlens, ref_logp, beta, kind, label_smoothing, margin, average,
+                                  logit_scale, grad_scale, dlogits, want_grad, ws, _raw(stream))
+    _keep(stream, *out, ws)
+    return PreferenceOut(*out)
 
 
 @dataclass
@@ -602,18 +535,12 @@ def policy_loss(logits, targets, advantages, weights, old_logp, ref_logp, clip_l
 
     advantages, weights fp32 [M]; old_logp, ref_logp fp32 [M] or None (ratio 1, no KL term).
     dlogits may be the logits themselves; with want_grad=False and no dlogits, the loss alone."""
-    dt, M, V, ld, dev = _rows(logits, "logits")
-    f32, m = torch.float32, (M,)
-    py = _need(targets, "targets", torch.int64, m, dev)
-    pa, pw = _need(advantages, "advantages", f32, m, dev), _need(weights, "weights", f32, m, dev)
-    pl, pr = _opt(old_logp, "old_logp", f32, m, dev), _opt(ref_logp, "ref_logp", f32, m, dev)
-    dlogits, pd, ldd = _grad_rows(dlogits, logits, want_grad)
-    ps, ns, po, logp, stats = _loss_out(logits, M, 4, ws, stream)
-    _keep(stream, dlogits)
-    _check("policy_loss", lib().policy_loss(
-        logits.data_ptr(), dt, M, V, ld, logit_scale, py, pa, pw, pl, pr, clip_low, clip_high, kl_coef, grad_scale,
-        po + 4 * M, po, pd, ldd, ps, ns, _stream(stream)))
-    return PolicyOut(stats, logp, dlogits)
+    if stream is not None and ws is None:
+        ws = loss_workspace(logits.shape[0], logits.device)
+    out = _step().policy_loss(logits, targets, advantages, weights, old_logp, ref_logp, clip_low, clip_high, kl_coef,
+                              logit_scale, grad_scale, dlogits, want_grad, ws, _raw(stream))
+    _keep(stream, *out, ws)
+    return PolicyOut(*out)
 
 
 def qlora_device_status(reset: bool = True) -> int:
