@@ -45,24 +45,30 @@ __device__ __forceinline__ float scale_of(uint32_t b) {
     return __uint_as_float(bits);
 }
 
-// four codes (one 32-bit word) times s, as two packed bf16 pairs
+// the values of four codes (one 32-bit word)
 template <bool E4M3>
-__device__ __forceinline__ void restore4(uint32_t w, float s, uint32_t& lo, uint32_t& hi) {
-    float v0, v1, v2, v3;
+__device__ __forceinline__ void values4(uint32_t w, float (&v)[4]) {
     if (E4M3) {
         const float2 a = adam::e4m3x2_to_f32(w), b = adam::e4m3x2_to_f32(w >> 16);
-        v0 = a.x; v1 = a.y; v2 = b.x; v3 = b.y;
+        v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
     } else {
         // two's complement byte c: bits of 2^23 + (c + 128), minus 2^23 + 128, is c
         const uint32_t u = w ^ 0x80808080u;
         constexpr float kBias = 8388608.f + 128.f;
-        v0 = __uint_as_float(prmt(u, 0x4b000000u, 0x7540u)) - kBias;
-        v1 = __uint_as_float(prmt(u, 0x4b000000u, 0x7541u)) - kBias;
-        v2 = __uint_as_float(prmt(u, 0x4b000000u, 0x7542u)) - kBias;
-        v3 = __uint_as_float(prmt(u, 0x4b000000u, 0x7543u)) - kBias;
+        v[0] = __uint_as_float(prmt(u, 0x4b000000u, 0x7540u)) - kBias;
+        v[1] = __uint_as_float(prmt(u, 0x4b000000u, 0x7541u)) - kBias;
+        v[2] = __uint_as_float(prmt(u, 0x4b000000u, 0x7542u)) - kBias;
+        v[3] = __uint_as_float(prmt(u, 0x4b000000u, 0x7543u)) - kBias;
     }
-    lo = pack_bf16x2(v0 * s, v1 * s);
-    hi = pack_bf16x2(v2 * s, v3 * s);
+}
+
+// four codes times s, as two packed bf16 pairs
+template <bool E4M3>
+__device__ __forceinline__ void restore4(uint32_t w, float s, uint32_t& lo, uint32_t& hi) {
+    float v[4];
+    values4<E4M3>(w, v);
+    lo = pack_bf16x2(v[0] * s, v[1] * s);
+    hi = pack_bf16x2(v[2] * s, v[3] * s);
 }
 
 // n8: chunks of 8 values (a multiple of 4: blocks of 32 are whole)

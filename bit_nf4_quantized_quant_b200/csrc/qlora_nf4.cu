@@ -686,9 +686,9 @@ int sk_cluster(int64_t tiles, int64_t nred, int smem_per_cta, int sms) {
     return z;
 }
 
-template <typename... KArgs>
-int launch_sk(void (*kern)(KArgs...), int z, int64_t tiles, int smem, cudaStream_t st, const CUtensorMap& tmP,
-              const CUtensorMap& tmQ, const sk::Args& a) {
+template <typename KA>
+int launch_sk(void (*kern)(CUtensorMap, CUtensorMap, KA), int z, int64_t tiles, int smem, cudaStream_t st,
+              const CUtensorMap& tmP, const CUtensorMap& tmQ, const std::remove_const_t<KA>& a) {
     const int64_t ctas = tiles * z;
     if (ctas > 0x7fffffffLL) return QLORA_ERR_SHAPE;
     cudaLaunchConfig_t cfg{};
@@ -771,6 +771,49 @@ int run_colk(const uint16_t* P, int64_t M, int64_t L, const uint16_t* Q, int64_t
     return launch_sk(sk::k_colk<128>, z, tiles, smem, st, tmP, tmQ, a);
 }
 
+template <int JQ, bool E4M3>
+int launch_colk8(const CUtensorMap& tmP, const CUtensorMap& tmQ, const sk::Args8& a, int z, cudaStream_t st) {
+    static std::atomic<int> set[64];
+    constexpr int smem = sk::Lay8<JQ>::SMEM_ALLOC;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QLORA_ERR_DEVICE;
+    if (set[dev].load() == 0) {
+        if (cudaFuncSetAttribute(sk::k_colk8<JQ, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess)
+            return QLORA_ERR_LAUNCH;
+        set[dev].store(1);
+    }
+    return launch_sk(sk::k_colk8<JQ, E4M3>, z, cdiv(a.a.L, sk::kCols8), smem, st, tmP, tmQ, a);
+}
+
+// run_colk with P an 8-bit checkpoint and trans_out (dA): out (j, l) for j < jout.
+// The cluster size is the one that run_colk takes for the restored tensor, so
+// that the sums have the same order.
+int run_colk8(const act8_tensor& P, const uint16_t* Q, int64_t qn, int pair, int jout, const FinishArgs& f, int sms,
+              cudaStream_t st, bool wait_end) {
+    const int64_t M = P.M, L = P.K;
+    const int jq = sk_jq(qn);
+    const int box = jq > 64 ? 64 : jq;
+    CUtensorMap tmP, tmQ;
+    if (!make_map_2d(&tmP, CU_TENSOR_MAP_DATA_TYPE_UINT8, P.codes, L, M, L, sk::kCols8, 64,
+                     CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_2d(&tmQ, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Q, qn, M, qn * 2, box, 64, sk_swizzle(box * 2)))
+        return QLORA_ERR_LAUNCH;
+    sk::Args8 a{};
+    a.scales = P.scales;
+    a.a.M = M; a.a.L = L; a.a.nred = cdiv(M, sk::TILE); a.a.pair = pair; a.a.jout = jout; a.a.trans_out = 1;
+    a.a.wait_end = wait_end ? 1 : 0;
+    a.a.f = f;
+    const int smem = jq == 32 ? sk::Lay<32>::SMEM_ALLOC : jq == 64 ? sk::Lay<64>::SMEM_ALLOC
+                                                                   : sk::Lay<128>::SMEM_ALLOC;
+    const int z = sk_cluster(cdiv(L, sk::TILE), a.a.nred, smem, sms);
+    a.a.ns = (int)cdiv(a.a.nred, z);
+    const bool e4 = P.fmt == QLORA_ACT8_E4M3;      // qn = 2 rp >= 32
+    if (jq == 32) return e4 ? launch_colk8<32, true>(tmP, tmQ, a, z, st) : launch_colk8<32, false>(tmP, tmQ, a, z, st);
+    if (jq == 64) return e4 ? launch_colk8<64, true>(tmP, tmQ, a, z, st) : launch_colk8<64, false>(tmP, tmQ, a, z, st);
+    return e4 ? launch_colk8<128, true>(tmP, tmQ, a, z, st) : launch_colk8<128, false>(tmP, tmQ, a, z, st);
+}
+
 // Tokens at or below this count take the small-M (GEMV-shaped) kernels.
 constexpr int64_t kSmallMaxM = 32;
 
@@ -799,8 +842,8 @@ int compute_T(const Plan& p, const uint16_t* X, const uint16_t* A, float s, uint
 
 // Small-M T = X A^T into T32 (and the caller's bf16 T_out): programmatic
 // launch behind the forward GEMV, plain launch in the backward's recompute.
-int small_T(const Plan& p, const uint16_t* X, const uint16_t* A, uint16_t* T_out, uint8_t* ws, cudaStream_t st,
-            bool pdl) {
+int small_T(const Plan& p, const uint16_t* X, const act8_tensor* x8, const uint16_t* A, uint16_t* T_out, uint8_t* ws,
+            cudaStream_t st, bool pdl) {
     LoraDownArgs d{};
     d.X = X; d.A = A; d.M = p.M; d.K = p.K; d.r = p.r; d.rp = p.rp;
     d.kc = pdl ? p.TKC : 1;             // the forward's split sums are added by the finish kernel
@@ -811,6 +854,13 @@ int small_T(const Plan& p, const uint16_t* X, const uint16_t* A, uint16_t* T_out
     void (*kern)(LoraDownArgs) = mg == 1 ? k_lora_down_small<1> : mg == 2 ? k_lora_down_small<2>
                                 : k_lora_down_small<4>;
     if (pdl) return launch_pdl(kern, grid, block, 0, st, d);
+    if (x8) {
+        d.xc = x8->codes; d.xs = x8->scales;
+        if (x8->fmt == QLORA_ACT8_E4M3)
+            kern = mg == 1 ? k_lora_down_small<1, 2> : mg == 2 ? k_lora_down_small<2, 2> : k_lora_down_small<4, 2>;
+        else
+            kern = mg == 1 ? k_lora_down_small<1, 1> : mg == 2 ? k_lora_down_small<2, 1> : k_lora_down_small<4, 1>;
+    }
     kern<<<grid, block, 0, st>>>(d);
     note_launch();
     return launch_status();
@@ -885,7 +935,7 @@ int launch_gemv_ntt(const Plan& p, const nf4dq_weight* w, const uint16_t* X, con
     int rc = launch_pdl(gmv::k_nf4_gemv<NTT>, dim3((unsigned)ctas), dim3(gmv::kThreads), (size_t)C::SMEM_ALLOC, st,
                         tmP, a, tables(w->quant_type));
     if (rc != QLORA_OK) return rc;
-    rc = small_T(p, Xl, A, nullptr, wsb, st, true);
+    rc = small_T(p, Xl, nullptr, A, nullptr, wsb, st, true);
     if (rc != QLORA_OK) return rc;
     gmv::FinishArgs f{};
     f.slots = a.slots; f.M = p.M; f.N = N; f.nks = a.nks; f.ctas = a.ctas; f.NT = C::NT; f.units = a.units;
@@ -914,13 +964,13 @@ int small_fwd(const Plan& p, const uint16_t* X, const uint16_t* Xl, const nf4dq_
 
 // Small-M backward: [T], U partials + dB, the fused dY W' kernel (overlapping
 // the U / dB kernel), then dX = dY W' + s U A and dA.
-int small_bwd(const Plan& p, const uint16_t* Xl, const uint16_t* dY, const nf4dq_weight* w, const uint16_t* A,
+int small_bwd(const Plan& p, const uint16_t* Xl, const act8_tensor* x8, const uint16_t* dY, const nf4dq_weight* w, const uint16_t* A,
               const uint16_t* B, float scaling, const uint16_t* T, uint16_t* dX, uint16_t* dA, uint16_t* dB,
               uint8_t* wsb, int sms, cudaStream_t st, const drop::Params* dp, const uint16_t* mask) {
     int rc = QLORA_OK;
     const float* T32 = nullptr;
     if (T == nullptr) {
-        rc = small_T(p, Xl, A, nullptr, wsb, st, false);
+        rc = small_T(p, Xl, x8, A, nullptr, wsb, st, false);
         if (rc != QLORA_OK) return rc;
         T32 = reinterpret_cast<const float*>(wsb + p.off_T32);
     }
@@ -942,6 +992,7 @@ int small_bwd(const Plan& p, const uint16_t* Xl, const uint16_t* dY, const nf4dq
     e.slots = ta.slots; e.NT = p.NT; e.nks = ta.nks; e.ctas = ta.ctas; e.units = ta.units;
     e.Upart = b.Upart; e.US = p.US; e.A = A; e.X = Xl;
     if (dp) { e.mask = mask; e.c = dp->c; }
+    if (x8) { e.xc = x8->codes; e.xs = x8->scales; e.xfmt = x8->fmt == QLORA_ACT8_E4M3 ? 2 : 1; }
     e.M = p.M; e.K = p.K; e.r = p.r; e.rp = p.rp; e.s = scaling; e.dX = dX; e.dA = dA;
     e.s_da = dp ? (float)((double)scaling * (double)dp->c) : scaling;
     return launch_pdl(k_bwd_small_end, dim3((unsigned)cdiv(p.K, kLoraThreads), (unsigned)(p.M + p.r)),
@@ -1321,7 +1372,10 @@ static int bwd_impl(const qlora_bf16* X, const act8_tensor* x8, const qlora_bf16
     if (ws_bytes < p.total + (dp ? dropout_bytes(M, K) : 0) + (x8 ? xb : 0)) return QLORA_ERR_WORKSPACE;
     cudaStream_t st = (cudaStream_t)stream;
     uint8_t* wsb = static_cast<uint8_t*>(ws);
-    if (x8) {
+    // a checkpoint is read by the kernels as it is, and restored into the workspace only for
+    // dropout's masked copy, ranks above 64, and T = X A^T of more than 32 tokens
+    const bool direct = x8 && !dp && (M <= kSmallMaxM || p.rp <= kSkMaxRp);
+    if (x8 && !(direct && (M <= kSmallMaxM || T != nullptr))) {
         uint16_t* xr = reinterpret_cast<uint16_t*>(wsb + p.total + (dp ? dropout_bytes(M, K) : 0));
         rc = launch_act8_dequant(x8, xr, st);
         if (rc != QLORA_OK) return rc;
@@ -1336,7 +1390,7 @@ static int bwd_impl(const qlora_bf16* X, const act8_tensor* x8, const qlora_bf16
         Xl = reinterpret_cast<const uint16_t*>(wsb + p.total);
     }
     if (M <= kSmallMaxM) {
-        rc = small_bwd(p, Xl, dY, w, A, B, scaling, T, dX, dA, dB, wsb, sms, st, dp, mask);
+        rc = small_bwd(p, Xl, direct ? x8 : nullptr, dY, w, A, B, scaling, T, dX, dA, dB, wsb, sms, st, dp, mask);
         if (rc == QLORA_OK) t_last_path = 1;
         return rc;
     }
@@ -1423,7 +1477,9 @@ static int bwd_impl(const qlora_bf16* X, const act8_tensor* x8, const qlora_bf16
         f.Iout = r; f.Jiter = K; f.row_pair = p.rp;
         f.o1 = dA; f.s1i = K; f.s1j = 1; f.J1 = K; f.J1pad = K;
         f.alpha1 = dp ? (float)((double)scaling * (double)dp->c) : scaling;
-        if (p.rp <= kSkMaxRp)
+        if (direct)
+            rc = run_colk8(*x8, Uhl, 2 * p.rp, p.rp, r, f, sms, st, beside);
+        else if (p.rp <= kSkMaxRp)
             rc = run_colk(Xl, M, K, Uhl, 2 * p.rp, 2 * p.rp, p.rp, r, true, f, sms, st, beside);
         else
             rc = run_gemm<false, false>(Uhl, 2 * p.rp, Xl, K, 2 * p.rp, K, M, 2 * p.rp, K, p.zA, p.kA, part, f, sms,

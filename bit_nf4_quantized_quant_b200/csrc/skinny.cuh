@@ -32,6 +32,10 @@
 //    kernel computing U has completed), not at all at the start: the kernel
 //    then runs beside the one before it on the SMs that one leaves free, and
 //    one CTA waits for it before exiting, so this grid completes after it.
+//  * dA from an 8-bit checkpoint of X (k_colk8): the codes come through the
+//    ring as they are (64 tokens x 128 columns, a quarter of the bytes of the
+//    bf16 tiles per column) and become bf16 in registers, on the way into the
+//    multiply-adds; see there.
 //  * Every mbarrier wait is bounded (an expired wait raises the CTA's abort
 //    flag and the device status); every thread still takes both cluster
 //    barriers, so an aborting CTA never strands its cluster.
@@ -40,6 +44,7 @@
 #include "common.cuh"
 #include "lora.cuh"
 #include "tc_gemm.cuh"
+#include "act8.cuh"
 
 namespace qnf4 {
 namespace sk {
@@ -50,6 +55,7 @@ constexpr int TILE = 64;                          // a P tile: 64 rows x 64 bf16
 constexpr int kStages = 6;
 constexpr int P_BYTES = TILE * TILE * 2;          // 8192
 constexpr int kMaxCluster = 8;
+constexpr int act8_block = QLORA_ACT8_BLOCK;
 
 template <int JQ>
 struct Lay {
@@ -401,6 +407,226 @@ template <int JQ>
 __global__ void __launch_bounds__(kThreads) k_colk(const __grid_constant__ CUtensorMap tmP,
                                                    const __grid_constant__ CUtensorMap tmQ, const Args a) {
     run<true, 0, JQ>(&tmP, &tmQ, a);
+}
+
+// ---------------------------------------------------------------------------
+// dA^T = X^T U with X an 8-bit checkpoint
+// ---------------------------------------------------------------------------
+// As k_colk with trans_out, on tiles of 64 tokens x 128 columns of codes.  A
+// consumer warp takes 32 columns, one scale block wide: lane (g, q) = (lane / 4,
+// lane % 4) reads 32-bit words of 4 adjacent columns 4 g .. 4 g + 3 for the
+// tokens that its fragments of the m16n8k16 product need, so that column
+// 4 g + i is row g + 8 (i & 1) of the warp's row tile i / 2 (the outputs are
+// put back in order where they are stored), and the four rows that the lanes of
+// one load touch differ in bits 1 and 2, which the 128-byte swizzle spreads
+// over the banks.  A token's scale is a byte per warp, loaded by lanes two
+// stages ahead and handed round by shuffles.  The split over the cluster, the
+// order of the sums and the operands are those of k_colk on the restored
+// tensor, and so is the result, bit for bit.
+constexpr int kCols8 = 128;
+constexpr int P8_BYTES = TILE * kCols8;
+constexpr int kStages8 = 4;
+
+template <int JQ>
+struct Lay8 {
+    static constexpr int Q_BYTES = JQ * 128;
+    static constexpr int STAGE = P8_BYTES + Q_BYTES;
+    static constexpr int RT_LD = kCols8 + 4;              // fp32 pitch of the transposed partial tile [JQ][128]
+    // the partial tile takes the place of the ring, which has been read by then
+    static constexpr int RING = kStages8 * STAGE, RED = JQ * RT_LD * 4;
+    static constexpr int OFF_BAR = RING > RED ? RING : (RED + 1023) / 1024 * 1024;
+    static constexpr int SMEM_ALLOC = OFF_BAR + 2 * kStages8 * 8 + 16 + 1024;
+};
+
+struct Args8 {
+    Args a;
+    const uint8_t* scales;       // [M, K / 32]
+};
+
+template <int JQ, bool E4M3>
+__global__ void __launch_bounds__(kThreads) k_colk8(const __grid_constant__ CUtensorMap tmP,
+                                                    const __grid_constant__ CUtensorMap tmQ, const Args8 aa) {
+    using LY = Lay8<JQ>;
+    constexpr int QSPAN = JQ >= 64 ? 128 : JQ * 2;
+    const Args& a = aa.a;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const uint32_t sbase = smem_u32(base);
+    const uint32_t bar0 = sbase + LY::OFF_BAR;
+    auto full = [&](int i) { return bar0 + 8 * i; };
+    auto empty = [&](int i) { return bar0 + 8 * (kStages8 + i); };
+    volatile int* s_abort = reinterpret_cast<volatile int*>(base + LY::OFF_BAR + 2 * kStages8 * 8);
+    float* red = reinterpret_cast<float*>(base);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    uint32_t zc;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(zc));
+    const int z = (int)zc;
+    const int64_t t0 = (int64_t)(blockIdx.x / zc) * kCols8;
+    const int64_t s_begin = (int64_t)rank * a.ns;
+    const int n = (int)(s_begin >= a.nred ? 0 : (a.nred - s_begin < a.ns ? a.nred - s_begin : a.ns));
+
+    if (a.wait_end) grid_dep_launch();
+    if (tid == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmP)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmQ)) : "memory");
+        for (int i = 0; i < kStages8; ++i) {
+            tc::mbar_init(full(i), 1);
+            tc::mbar_init(empty(i), kCons);
+        }
+        *s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    if (!a.wait_end) {
+        grid_dep_wait();
+        grid_dep_launch();
+    }
+
+    float acc[2][JQ / 8][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < JQ / 8; ++t) acc[h][t][0] = acc[h][t][1] = acc[h][t][2] = acc[h][t][3] = 0.f;
+    const int g = lane >> 2, q = lane & 3;
+    if (warp == kCons) {
+        // ---------------------------------------------------------------- producer
+        if (lane == 0) {
+            int issued = 0;
+            bool ok = true;
+            for (int s = 0; s < n; ++s) {
+                const int st = s % kStages8, ph = (s / kStages8) & 1;
+                if (!tc::mbar_wait(empty(st), ph ^ 1, s_abort)) { ok = false; break; }
+                const uint32_t dst = sbase + st * LY::STAGE;
+                const int rpos = (int)((s_begin + s) * TILE);
+                tc::mbar_expect_tx(full(st), LY::STAGE);
+                tc::tma_load_2d(dst, &tmP, full(st), (int)t0, rpos);
+                tc::tma_load_2d(dst + P8_BYTES, &tmQ, full(st), 0, rpos);
+                if (JQ == 128) tc::tma_load_2d(dst + P8_BYTES + 8192, &tmQ, full(st), 64, rpos);
+                ++issued;
+            }
+            if (!ok)
+                for (int k = 1; k <= kStages8 && k <= issued; ++k)
+                    tc::mbar_drain(full((issued - k) % kStages8), ((issued - k) / kStages8) & 1);
+        }
+    } else {
+        // ---------------------------------------------------------------- consumers
+        const int mi = lane >> 3, rr = lane & 7;
+        const int64_t sk = a.L / act8_block, cb = t0 / act8_block + warp;       // scale columns, this warp's one
+        auto scale = [&](int s, int half) -> uint32_t {
+            const int64_t m = (s_begin + s) * TILE + 32 * half + lane;
+            return s < n && m < a.M && cb < sk ? aa.scales[m * sk + cb] : 0u;
+        };
+        uint32_t next[2][2] = {{scale(0, 0), scale(0, 1)}, {scale(1, 0), scale(1, 1)}};
+        for (int s = 0; s < n; ++s) {
+            const int st = s % kStages8, ph = (s / kStages8) & 1;
+            const float sc0 = act8::scale_of(next[0][0]), sc1 = act8::scale_of(next[0][1]);
+            next[0][0] = next[1][0]; next[0][1] = next[1][1];
+            next[1][0] = scale(s + 2, 0); next[1][1] = scale(s + 2, 1);
+            if (!tc::mbar_wait(full(st), ph, s_abort)) break;
+            const uint32_t pb = sbase + st * LY::STAGE, qb = pb + P8_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                uint32_t w[4];
+                float ts[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 16 * kk + 8 * (i >> 1) + 2 * q + (i & 1);
+                    w[i] = lds_u32(pb + swz(row, 2 * warp + (g >> 2), 128) + 4 * (g & 3));
+                    ts[i] = __shfl_sync(0xffffffffu, kk < 2 ? sc0 : sc1, row & 31);
+                }
+                // af[c][h]: column 4 g + c, tokens of words 2 h and 2 h + 1
+                uint32_t af[4][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v[2][4];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) act8::values4<E4M3>(w[2 * h + e], v[e]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        af[c][h] = pack_bf16x2(v[0][c] * ts[2 * h], v[1][c] * ts[2 * h + 1]);
+                }
+                const int qrow = 16 * kk + rr + (mi & 1) * 8;
+#pragma unroll
+                for (int bb = 0; bb < JQ / 16; ++bb) {
+                    const int cj = 2 * bb + (mi >> 1);
+                    const uint32_t addr = JQ == 128 ? qb + (uint32_t)((cj >> 3) * 8192) + swz(qrow, cj & 7, 128)
+                                                    : qb + swz(qrow, cj, QSPAN);
+                    uint32_t b0, b1, b2, b3;
+                    ldsm_x4_t(addr, b0, b1, b2, b3);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        mma_bf16_16816(acc[h][2 * bb], af[2 * h][0], af[2 * h + 1][0], af[2 * h][1], af[2 * h + 1][1],
+                                       b0, b1);
+                        mma_bf16_16816(acc[h][2 * bb + 1], af[2 * h][0], af[2 * h + 1][0], af[2 * h][1],
+                                       af[2 * h + 1][1], b2, b3);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(empty(st));
+        }
+    }
+    __syncthreads();                      // the ring has been read
+    if (warp < kCons) {
+        // rows j = 8 t + 2 q (+ 1), columns 32 warp + 4 g + 2 h (+ 1)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int t = 0; t < JQ / 8; ++t) {
+                float* r0 = red + (8 * t + 2 * q) * LY::RT_LD + 32 * warp + 4 * g + 2 * h;
+                *reinterpret_cast<float2*>(r0) = make_float2(acc[h][t][0], acc[h][t][2]);
+                *reinterpret_cast<float2*>(r0 + LY::RT_LD) = make_float2(acc[h][t][1], acc[h][t][3]);
+            }
+    }
+    __syncthreads();
+    cluster_sync();                       // every partial tile of the cluster is in place
+
+    const uint32_t red_s = smem_u32(red);
+    const FinishArgs& f = a.f;
+    auto sum8 = [&](uint32_t off, float (&v)[8]) {
+        float4 lo[kMaxCluster], hi[kMaxCluster];
+#pragma unroll
+        for (int p = 0; p < kMaxCluster; ++p)
+            if (p < z) {
+                const uint32_t ad = mapa(off, (uint32_t)p);
+                lo[p] = ld_dsmem_v4(ad);
+                hi[p] = ld_dsmem_v4(ad + 16);
+            }
+#pragma unroll
+        for (int p = 0; p < kMaxCluster; ++p)
+            if (p < z) {
+                v[0] += lo[p].x; v[1] += lo[p].y; v[2] += lo[p].z; v[3] += lo[p].w;
+                v[4] += hi[p].x; v[5] += hi[p].y; v[6] += hi[p].z; v[7] += hi[p].w;
+            }
+    };
+    const int G = a.jout * (kCols8 / 8);
+    const int g_lo = (int)((int64_t)G * rank / z), g_hi = (int)((int64_t)G * (rank + 1) / z);
+    const bool vec = f.s1i % 8 == 0 && (reinterpret_cast<uintptr_t>(f.o1) & 15) == 0;
+    for (int e = g_lo + tid; e < g_hi; e += kThreads) {
+        const int j = e / (kCols8 / 8), l_loc = 8 * (e - j * (kCols8 / 8));
+        const int64_t l0 = t0 + l_loc;
+        if (l0 >= a.L) continue;
+        const uint32_t off = red_s + (uint32_t)((j * LY::RT_LD + l_loc) * 4);
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        sum8(off, v);
+        if (a.pair > 0) sum8(off + (uint32_t)(a.pair * LY::RT_LD * 4), v);
+        uint32_t b[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            b[c] = pack_bf16x2(__fmul_rn(f.alpha1, __fmul_rn(v[2 * c], f.pre)),
+                               __fmul_rn(f.alpha1, __fmul_rn(v[2 * c + 1], f.pre)));
+        uint16_t* d = f.o1 + (int64_t)j * f.s1i + l0;
+        if (vec) {                        // L is a multiple of 64: 8 columns are in or out together
+            *reinterpret_cast<uint4*>(d) = make_uint4(b[0], b[1], b[2], b[3]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) d[c] = (uint16_t)((c & 1) ? (b[c >> 1] >> 16) : (b[c >> 1] & 0xffffu));
+        }
+    }
+    cluster_sync();                       // no CTA leaves while its partial tile may still be read
+    if (a.wait_end && blockIdx.x == gridDim.x - 1 && tid == 0) grid_dep_wait();
 }
 
 }  // namespace sk

@@ -19,6 +19,7 @@
 #pragma once
 #include "common.cuh"
 #include "dropout.cuh"
+#include "act8.cuh"
 
 namespace qnf4 {
 
@@ -35,6 +36,8 @@ struct LoraDownArgs {
     int kc;                  // K splits: split z sums the 8-wide chunks [z nch / kc, (z + 1) nch / kc)
     float* T32;              // [kc][M, rp] fp32 partial sums (columns >= r not written)
     uint16_t* T_out;         // [M, r] bf16 copy for the caller (kc == 1 only), or null
+    const uint8_t* xc;       // X as an 8-bit checkpoint (XF != 0): codes [M, K] and
+    const uint8_t* xs;       // scale bytes [M, K / 32]
 };
 
 // K splits of the forward's T: about two 8-wide chunks per thread and split.
@@ -59,11 +62,13 @@ __device__ __forceinline__ float dot8_bf16(const uint4& x, const uint4& y, float
 // lets the finish kernel launch at once, and its first CTA waits for the
 // GEMV before it ends, so that this grid's completion implies the GEMV's
 // (the other CTAs exit as soon as their sums are written).  Launched plainly
-// (the backward's recompute, one split) the wait returns at once.
+// (the backward's recompute, one split) the wait returns at once.  XF: X is
+// bf16 (0) or an 8-bit checkpoint (1: int8, 2: E4M3), whose values are exact in
+// bf16, so that T is that of the restored tensor.
 constexpr int kDownThreads = 128;
 
-template <int MG>
-__global__ void __launch_bounds__(kDownThreads, 16) k_lora_down_small(LoraDownArgs a) {
+template <int MG, int XF = 0>
+__global__ void __launch_bounds__(kDownThreads, XF ? 8 : 16) k_lora_down_small(LoraDownArgs a) {
     grid_dep_launch();
     __shared__ float s_red[kDownThreads / 32][MG];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -81,7 +86,19 @@ __global__ void __launch_bounds__(kDownThreads, 16) k_lora_down_small(LoraDownAr
         const uint4 av = ldg_cg_v4(ar + c);
 #pragma unroll
         for (int mm = 0; mm < MG; ++mm)
-            if (mm < mn) acc[mm] = dot8_bf16(ldg_cg_v4(xr + mm * nch + c), av, acc[mm]);
+            if (mm < mn) {
+                if (XF == 0) {
+                    acc[mm] = dot8_bf16(ldg_cg_v4(xr + mm * nch + c), av, acc[mm]);
+                } else {
+                    const int64_t e8 = (m0 + mm) * nch + c;
+                    const uint2 q = *reinterpret_cast<const uint2*>(a.xc + 8 * e8);
+                    const float sc = act8::scale_of(a.xs[e8 >> 2]);
+                    uint4 xv;
+                    act8::restore4<XF == 2>(q.x, sc, xv.x, xv.y);
+                    act8::restore4<XF == 2>(q.y, sc, xv.z, xv.w);
+                    acc[mm] = dot8_bf16(xv, av, acc[mm]);
+                }
+            }
     }
 #pragma unroll
     for (int mm = 0; mm < MG; ++mm) {
@@ -272,6 +289,9 @@ struct BwdEndArgs {
     const uint16_t* mask;    // LoRA dropout: keep bits of [M, K] (the LoRA term of dX is masked, keep * c,
                              // and X above is then X * keep); null without dropout
     float c;                 // scale of kept values
+    const uint8_t* xc;       // X as an 8-bit checkpoint (xfmt != 0: 1 int8, 2 E4M3): codes [M, K] and
+    const uint8_t* xs;       // scale bytes [M, K / 32]
+    int xfmt;
 };
 
 // The CTA that owns unit u under k_tcs_gemm's even split of U units over C
@@ -333,7 +353,18 @@ __global__ void __launch_bounds__(kLoraThreads) k_bwd_small_end(BwdEndArgs a) {
     } else {
         const int i = y - (int)a.M;
         float v = 0.f;
-        for (int64_t m = 0; m < a.M; ++m) v = __fmaf_rn(s_u[m], bf16lo_to_f32(a.X[m * a.K + k]), v);
+        if (a.xfmt == 0) {
+            for (int64_t m = 0; m < a.M; ++m) v = __fmaf_rn(s_u[m], bf16lo_to_f32(a.X[m * a.K + k]), v);
+        } else {
+            for (int64_t m = 0; m < a.M; ++m) {
+                const int64_t e = m * a.K + k;
+                const uint32_t c = a.xc[e];
+                const float x = a.xfmt == 2 ? adam::e4m3x2_to_f32(c).x : (float)(int8_t)c;
+                // rounded to bf16 like the restored tensor (exact but for the smallest scales)
+                const uint32_t xb = pack_bf16x2(x * act8::scale_of(a.xs[e >> 5]), 0.f);
+                v = __fmaf_rn(s_u[m], bf16lo_to_f32(xb), v);
+            }
+        }
         a.dA[(int64_t)i * a.K + k] = (uint16_t)(pack_bf16x2(a.s_da * v, 0.f) & 0xffffu);
     }
 }
