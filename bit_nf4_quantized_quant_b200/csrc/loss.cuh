@@ -586,55 +586,54 @@ struct GradArgs {
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;                     // 16-byte vectors per thread
 
-// One chunk of kGradThreads * kGradVecs vectors of a row per CTA, the last
-// rows first: those are what the forward pass has left in L2.
-template <typename T>
-__global__ void __launch_bounds__(kGradThreads) k_dlogits(const GradArgs a) {
+// One chunk of kGradThreads * kGradVecs vectors of row `row`: coef() is called
+// once by every thread, with the chunk's loads under way, and gives
+// d loss / d logp of the row (a row without a target is zeroed without it).
+template <typename T, typename Coef>
+__device__ __forceinline__ void grad_chunk(const GradArgs& a, int64_t row, int ch, Coef coef) {
     constexpr int N = El<T>::N;
-    grid_dep_wait();
-    grid_dep_launch();
-    const int row_b = blockIdx.x / (unsigned)a.chunks, ch = blockIdx.x - row_b * a.chunks;
-    const int64_t row = a.M - 1 - row_b;
     const T* x = static_cast<const T*>(a.logits) + row * a.ld;
     T* o = static_cast<T*>(a.out) + row * a.ldo;
     const int64_t y64 = a.targets[row];
-    const float dl = a.dlogp[row];
     const float2 st = a.stats[row];
     const int y = y64 >= 0 && y64 < a.V ? (int)y64 : -1;
-    const float g = y >= 0 ? dl * a.tau : 0.f;
     const int tid = threadIdx.x;
     constexpr int cv = kGradThreads * kGradVecs;
     const bool careful = !(st.y > 0.f);          // (r, -S)
+    const bool same = (((uint32_t)reinterpret_cast<uintptr_t>(x) ^ (uint32_t)reinterpret_cast<uintptr_t>(o)) & 15) == 0;
+    const Row<T> sp(x, a.V);
+    const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
+    uint4* ov = reinterpret_cast<uint4*>(o + sp.head);
+    const int i0 = ch * cv + tid;
+    uint4 v[kGradVecs];
+    if (y >= 0 && same) {
+#pragma unroll
+        for (int u = 0; u < kGradVecs; ++u)
+            v[u] = i0 + u * kGradThreads < sp.nv ? ld_v4(xv + i0 + u * kGradThreads) : make_uint4(0, 0, 0, 0);
+    }
+    const float g = y >= 0 ? coef() * a.tau : 0.f;
     const float q = -g / (careful ? -st.y : st.y);
     auto one = [&](float l) { return q * ex2(careful ? (l - st.x) * a.c : fmaf(l, a.c, -st.x)); };
     auto put = [&](int e) {
-        const float f = one(El<T>::get(x[e]));
-        o[e] = El<T>::put(g == 0.f ? 0.f : e == y ? f + g : f);
+        const float f = g == 0.f ? 0.f : one(El<T>::get(x[e]));
+        o[e] = El<T>::put(g != 0.f && e == y ? f + g : f);
     };
-    if ((((uint32_t)reinterpret_cast<uintptr_t>(x) ^ (uint32_t)reinterpret_cast<uintptr_t>(o)) & 15) != 0) {
+    if (!same) {
         // the two rows cross 16-byte boundaries at different elements
         const int e1 = (ch + 1) * cv * N < a.V ? (ch + 1) * cv * N : a.V;
         for (int e = ch * cv * N + tid; e < e1; e += kGradThreads) put(e);
         return;
     }
-    const Row<T> sp(x, a.V);
-    const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
-    uint4* ov = reinterpret_cast<uint4*>(o + sp.head);
-    const int i0 = ch * cv + tid;
     if (ch == 0) {
         const int e = tid < sp.head ? tid : tid >= 8 && tid < 8 + sp.tail ? a.V - sp.tail + tid - 8 : -1;
         if (e >= 0) put(e);
     }
-    if (g == 0.f) {                              // padding, or a loss that is flat here: the vectors are not read
+    if (g == 0.f) {                              // padding, or a loss that is flat here
 #pragma unroll
         for (int u = 0; u < kGradVecs; ++u)
             if (i0 + u * kGradThreads < sp.nv) ov[i0 + u * kGradThreads] = make_uint4(0, 0, 0, 0);
         return;
     }
-    uint4 v[kGradVecs];
-#pragma unroll
-    for (int u = 0; u < kGradVecs; ++u)
-        v[u] = i0 + u * kGradThreads < sp.nv ? ld_v4(xv + i0 + u * kGradThreads) : make_uint4(0, 0, 0, 0);
     const int yv = y - sp.head;                  // the target among the vectors
     const int iy = yv >= 0 && yv < sp.nv * N ? yv / N : -1;
 #pragma unroll
@@ -651,6 +650,18 @@ __global__ void __launch_bounds__(kGradThreads) k_dlogits(const GradArgs a) {
         }
         if (i < sp.nv) ov[i] = El<T>::pack(f);
     }
+}
+
+// One chunk per CTA, the last rows first: those are what the forward pass has
+// left in L2.
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads) k_dlogits(const GradArgs a) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int row_b = blockIdx.x / (unsigned)a.chunks, ch = blockIdx.x - row_b * a.chunks;
+    const int64_t row = a.M - 1 - row_b;
+    const float d = a.dlogp[row];
+    grad_chunk<T>(a, row, ch, [&] { return d; });
 }
 
 // ---------------------------------------------------------------------------
@@ -686,32 +697,82 @@ __device__ __forceinline__ double warp_sum(double v) {
     return v;
 }
 
-// One pair by one warp (CTA = false) or by the whole CTA; returns the pair's loss.
-template <bool CTA>
-__device__ __forceinline__ double do_pair(const PairArgs& a, int64_t p, PairShared& sh) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int id = CTA ? threadIdx.x : lane, n = CTA ? kPairThreads : 32;
-    // the boundaries are device data: clamped, so that no value of theirs leads out of the arrays
-    auto at = [&](int64_t i, int64_t lo) {
-        int64_t c = a.cu[i];
-        c = c < lo ? lo : c;
-        return c < a.M ? c : a.M;
-    };
-    const int64_t s0 = at(2 * p, 0), s1 = at(2 * p + 1, s0), s2 = at(2 * p + 2, s1);
-    double t[4] = {0., 0., 0., 0.};              // chosen sum, rejected sum, chosen count, rejected count
+// Rows [s0, s1) and [s1, s2) of pair p.  The boundaries are device data: they
+// are clamped, so that no value of theirs leads out of the arrays.
+struct PairRows {
+    int64_t s0, s1, s2;
+    __device__ __forceinline__ PairRows(const PairArgs& a, int64_t p) {
+        auto at = [&](int64_t i, int64_t lo) {
+            int64_t c = a.cu[i];
+            c = c < lo ? lo : c;
+            return c < a.M ? c : a.M;
+        };
+        s0 = at(2 * p, 0);
+        s1 = at(2 * p + 1, s0);
+        s2 = at(2 * p + 2, s1);
+    }
+};
+
+// Thread id of n adds its rows to (chosen sum, rejected sum, chosen count, rejected count).
+__device__ __forceinline__ void pair_sums(const PairArgs& a, const PairRows& r, int id, int n, double (&t)[4]) {
+    t[0] = t[1] = t[2] = t[3] = 0.;
 #pragma unroll 4
-    for (int64_t i = s0 + id; i < s2; i += n) {
+    for (int64_t i = r.s0 + id; i < r.s2; i += n) {
         const int64_t y = a.targets[i];
         const double lp = a.lpd[i];
         const float rf = a.ref ? a.ref[i] : 0.f;
         if (y >= 0 && y < a.V) {
             const double d = lp - (double)rf;
-            if (i < s1) { t[0] += d; t[2] += 1.; }
+            if (i < r.s1) { t[0] += d; t[2] += 1.; }
             else { t[1] += d; t[3] += 1.; }
         }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) t[j] = warp_sum(t[j]);
+}
+
+// A pair's loss, its rewards over beta, and the gradient of a row of either sequence.
+struct PairTerms {
+    double loss, sc, sr;
+    float gc, gr;
+    __device__ __forceinline__ PairTerms(const PairArgs& a, const double (&t)[4]) {
+        const double dc = a.average && t[2] > 0. ? 1. / t[2] : 1., dr = a.average && t[3] > 0. ? 1. / t[3] : 1.;
+        sc = t[0] * dc;
+        sr = t[1] * dr;
+        const double delta = sc - sr, beta = (double)a.beta, eps = (double)a.smooth;
+        const double zz = beta * delta - (double)a.margin;
+        double g;                                // d loss / d delta
+        if (a.kind == QLORA_PREF_SIGMOID) {
+            const double e = exp(-fabs(zz)), sp = log1p(e);
+            loss = (1. - eps) * (sp + fmax(-zz, 0.)) + (eps != 0. ? eps * (sp + fmax(zz, 0.)) : 0.);
+            const double sg = zz >= 0. ? e / (1. + e) : 1. / (1. + e);      // sigmoid(-z)
+            g = beta * (eps * (1. - sg) - (1. - eps) * sg);
+        } else if (a.kind == QLORA_PREF_HINGE) {
+            loss = zz < 1. ? 1. - zz : zz == zz ? 0. : zz;
+            g = zz < 1. ? -beta : 0.;
+        } else {
+            const double q = delta - 0.5 / beta;
+            loss = q * q;
+            g = 2. * q;
+        }
+        const double k = g * (double)a.grad_scale / (double)a.P;
+        gc = (float)(k * dc);
+        gr = (float)(-k * dr);
+    }
+    __device__ __forceinline__ void put_rewards(const PairArgs& a, int64_t p) const {
+        a.rewards[2 * p] = (float)((double)a.beta * sc);
+        a.rewards[2 * p + 1] = (float)((double)a.beta * sr);
+    }
+};
+
+// One pair by one warp (CTA = false) or by the whole CTA; returns the pair's loss.
+template <bool CTA>
+__device__ __forceinline__ double do_pair(const PairArgs& a, int64_t p, PairShared& sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int id = CTA ? threadIdx.x : lane, n = CTA ? kPairThreads : 32;
+    const PairRows r(a, p);
+    double t[4];
+    pair_sums(a, r, id, n, t);
     if (CTA) {
         if (lane == 0)
             for (int j = 0; j < 4; ++j) sh.red[warp][j] = t[j];
@@ -720,34 +781,11 @@ __device__ __forceinline__ double do_pair(const PairArgs& a, int64_t p, PairShar
         for (int j = 0; j < 4; ++j) t[j] = warp_sum(sh.red[lane][j]);
         __syncthreads();
     }
-    const double dc = a.average && t[2] > 0. ? 1. / t[2] : 1., dr = a.average && t[3] > 0. ? 1. / t[3] : 1.;
-    const double sc = t[0] * dc, sr = t[1] * dr, delta = sc - sr;
-    const double beta = (double)a.beta, eps = (double)a.smooth;
-    const double zz = beta * delta - (double)a.margin;
-    double l, g;                                 // loss and d loss / d delta
-    if (a.kind == QLORA_PREF_SIGMOID) {
-        const double e = exp(-fabs(zz)), sp = log1p(e);
-        l = (1. - eps) * (sp + fmax(-zz, 0.)) + (eps != 0. ? eps * (sp + fmax(zz, 0.)) : 0.);
-        const double sg = zz >= 0. ? e / (1. + e) : 1. / (1. + e);      // sigmoid(-z)
-        g = beta * (eps * (1. - sg) - (1. - eps) * sg);
-    } else if (a.kind == QLORA_PREF_HINGE) {
-        l = zz < 1. ? 1. - zz : zz == zz ? 0. : zz;
-        g = zz < 1. ? -beta : 0.;
-    } else {
-        const double q = delta - 0.5 / beta;
-        l = q * q;
-        g = 2. * q;
-    }
-    if (id == 0) {
-        a.rewards[2 * p] = (float)(beta * sc);
-        a.rewards[2 * p + 1] = (float)(beta * sr);
-    }
-    if (a.dlogp) {
-        const double k = g * (double)a.grad_scale / (double)a.P;
-        const float gc = (float)(k * dc), gr = (float)(-k * dr);
-        for (int64_t i = s0 + id; i < s2; i += n) a.dlogp[i] = i < s1 ? gc : gr;
-    }
-    return l;
+    const PairTerms o(a, t);
+    if (id == 0) o.put_rewards(a, p);
+    if (a.dlogp)
+        for (int64_t i = r.s0 + id; i < r.s2; i += n) a.dlogp[i] = i < r.s1 ? o.gc : o.gr;
+    return o.loss;
 }
 
 // One cluster.  CTA c owns the pairs c, c + 8, ...: short ones go to its
@@ -806,6 +844,67 @@ __global__ void __launch_bounds__(kPairThreads) k_preference(const PairArgs a) {
         for (int q = 0; q < kPairCtas; ++q) v += sh.rank_loss[q];
         a.loss[0] = (float)(v / (double)a.P);
     }
+}
+
+// Pair losses and gradient of up to kFewRows rows and kFewPairs pairs in one
+// launch.  The first CTA takes the losses and the rewards, a pair a warp; each of the others takes a chunk of a
+// row, and adds up the row's pair itself while the chunk is on its way: a few
+// hundred values, for which a kernel of its own before this one costs more
+// (one pair of 61 x 32000: 16.5 us in three launches, 12 us in two).
+constexpr int kFewRows = 512, kFewPairs = 32;
+
+struct FewArgs {
+    PairArgs p;
+    GradArgs g;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads) k_preference_few(const FewArgs a) {
+    __shared__ double red[kGradThreads / 32][4];
+    __shared__ float s_d;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (blockIdx.x == 0) {
+        double acc = 0.;
+        for (int64_t p = warp; p < a.p.P; p += kGradThreads / 32) {
+            double t[4];
+            pair_sums(a.p, PairRows(a.p, p), lane, 32, t);
+            const PairTerms o(a.p, t);
+            if (lane == 0) o.put_rewards(a.p, p);
+            acc += o.loss;
+        }
+        if (lane == 0) red[warp][0] = acc;
+        __syncthreads();
+        if (tid == 0) {
+            double v = 0.;
+            for (int w = 0; w < kGradThreads / 32; ++w) v += red[w][0];
+            a.p.loss[0] = (float)(v / (double)a.p.P);
+        }
+        return;
+    }
+    const int b = blockIdx.x - 1, row = b / (unsigned)a.g.chunks, ch = b - row * a.g.chunks;
+    grad_chunk<T>(a.g, row, ch, [&] {
+        // sequences that begin at or before the row; the row is in the last of them
+        int seq = -1;
+        for (int64_t i = 0; i <= 2 * a.p.P; i += kGradThreads)
+            seq += __syncthreads_count(i + tid <= 2 * a.p.P && a.p.cu[i + tid] <= row);
+        if (seq < 0 || seq >= 2 * a.p.P) return 0.f;
+        const PairRows r(a.p, seq >> 1);
+        double t[4];
+        pair_sums(a.p, r, tid, kGradThreads, t);
+        if (lane == 0)
+            for (int j = 0; j < 4; ++j) red[warp][j] = t[j];
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) t[j] = warp_sum(lane < kGradThreads / 32 ? red[lane][j] : 0.);
+            const PairTerms o(a.p, t);
+            if (lane == 0) s_d = seq & 1 ? o.gr : o.gc;
+        }
+        __syncthreads();
+        return s_d;
+    });
 }
 
 // ---------------------------------------------------------------------------

@@ -1650,13 +1650,20 @@ int preference_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t
     a.lpd = lpd; a.ref = ref_logp; a.targets = targets; a.M = M; a.V = (int)V; a.P = P; a.cu = cu_seqlens;
     a.kind = kind; a.average = average != 0; a.beta = beta; a.smooth = label_smoothing; a.margin = margin;
     a.grad_scale = grad_scale; a.loss = loss; a.rewards = rewards; a.dlogp = dlogits ? dlogp : nullptr;
-    rc = launch_rows<loss::PairArgs>(loss::k_preference, 1, loss::kPairCtas, loss::kPairThreads, st, a);
-    if (rc != QLORA_OK || !dlogits) return rc;
     loss::GradArgs g{};
     g.logits = logits; g.M = M; g.V = (int)V; g.ld = ld; g.tau = logit_scale;
     float c_lo;
     split_c(logit_scale, &g.c, &c_lo);
     g.targets = targets; g.stats = stats; g.dlogp = dlogp; g.out = dlogits; g.ldo = ldd; g.chunks = (int)chunks;
+    if (dlogits && M <= loss::kFewRows && P <= loss::kFewPairs) {
+        const loss::FewArgs fa{a, g};
+        return dtype == QLORA_LOGITS_FP32
+                   ? launch_rows<loss::FewArgs>(loss::k_preference_few<float>, M * chunks + 1, 1, loss::kGradThreads, st, fa)
+                   : launch_rows<loss::FewArgs>(loss::k_preference_few<uint16_t>, M * chunks + 1, 1, loss::kGradThreads, st,
+                                                fa);
+    }
+    rc = launch_rows<loss::PairArgs>(loss::k_preference, 1, loss::kPairCtas, loss::kPairThreads, st, a);
+    if (rc != QLORA_OK || !dlogits) return rc;
     return dtype == QLORA_LOGITS_FP32
                ? launch_rows<loss::GradArgs>(loss::k_dlogits<float>, M * chunks, 1, loss::kGradThreads, st, g)
                : launch_rows<loss::GradArgs>(loss::k_dlogits<uint16_t>, M * chunks, 1, loss::kGradThreads, st, g);

@@ -354,8 +354,9 @@ QLORA_API int token_logprob(const void* logits, int dtype, int64_t M, int64_t V,
 
 /* Preference loss over P pairs of packed sequences: sequence i is rows
  * [cu_seqlens[i], cu_seqlens[i + 1]), pair p prefers sequence 2p to 2p + 1;
- * cu_seqlens [2P + 1] int32, ascending (device data: values are clamped to
- * [0, M] and to the one before).  Rows in no sequence get gradient 0.
+ * cu_seqlens [2P + 1] int32, ascending (device data: whatever they hold, the
+ * rows of a pair are clamped to [0, M] and to ascending order).  Rows in no
+ * sequence get gradient 0.
  *   S_i     = sum over the sequence's rows with a target of logp - ref_logp
  *             (ref_logp NULL: of logp), divided by their number with
  *             average != 0 (a sequence without any: 0)

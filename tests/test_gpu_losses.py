@@ -180,7 +180,8 @@ def _run_preference(seed, M, V, P, dtype, kind, eps, margin, average, ld=None, o
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("kind,eps,margin,average", KINDS)
-@pytest.mark.parametrize("M,V,P", [(2, 5, 1), (30, 129, 1), (60, 1000, 4), (200, 2048, 9), (70, 32001, 2)])
+@pytest.mark.parametrize("M,V,P", [(2, 5, 1), (30, 129, 1), (60, 1000, 4), (200, 2048, 9), (70, 32001, 2), (512, 70, 32),
+                                   (400, 129, 40), (513, 300, 5), (600, 1003, 33)])
 def test_preference(M, V, P, kind, eps, margin, average, dtype):
     _run_preference(M + V + kind, M, V, P, dtype, kind, eps, margin, average)
 
