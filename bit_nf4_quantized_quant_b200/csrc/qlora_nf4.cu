@@ -979,10 +979,17 @@ int small_bwd(const Plan& p, const uint16_t* Xl, const act8_tensor* x8, const ui
     b.dY = dY; b.B = B; b.T32 = T32; b.Tb = T; b.M = p.M; b.N = p.N; b.r = p.r; b.rp = p.rp; b.s = scaling;
     b.tscale = dp ? dp->c : 1.f;
     b.b_vec = (p.r % 8 == 0 && aligned16(B)) ? 1 : 0;
-    b.Upart = reinterpret_cast<float*>(wsb + p.off_Upart); b.US = p.US; b.rows_u = p.rows_u; b.dB = dB;
-    k_lora_bwd_small<<<(unsigned)(p.US + cdiv(p.N, kLoraThreads)), kLoraThreads, 0, st>>>(b);
-    note_launch();
-    rc = launch_status();
+    b.Upart = reinterpret_cast<float*>(wsb + p.off_Upart); b.US = p.US; b.u_ctas = (int)(p.US * cdiv(p.M, kUTok)); b.rows_u = p.rows_u; b.dB = dB;
+    // behind the T kernel (a plain launch: everything before it has completed) it starts at once, and
+    // only its dB CTAs wait for T
+    const dim3 grid((unsigned)(b.u_ctas + cdiv(p.N, kLoraThreads)));
+    if (T32) {
+        rc = launch_pdl(k_lora_bwd_small, grid, dim3(kLoraThreads), 0, st, b);
+    } else {
+        k_lora_bwd_small<<<grid, kLoraThreads, 0, st>>>(b);
+        note_launch();
+        rc = launch_status();
+    }
     if (rc != QLORA_OK) return rc;
     tcs::Args ta{};
     rc = launch_tcs_bwd(p, w, dY, wsb, sms, st, &ta);

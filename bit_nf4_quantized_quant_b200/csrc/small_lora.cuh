@@ -133,12 +133,13 @@ struct LoraBwdArgs {
     float tscale;            // scale of the T32 values (1 except under LoRA dropout; Tb is taken as is)
     int b_vec;               // B rows are 16-byte loadable (r % 8 == 0, B 16-byte aligned)
     float* Upart;            // [US][M][rp] fp32 partial U (columns >= r not written)
-    int US;                  // N splits of U; CTAs [0, US) compute U
+    int US;                  // N splits of U
+    int u_ctas;              // CTAs [0, u_ctas) compute U: US for each group of kUTok tokens
     int64_t rows_u;          // rows of B per split
     uint16_t* dB;            // [N, r] bf16
 };
 
-constexpr int kUTok = 4;     // tokens per pass of a U split
+constexpr int kUTok = 4;     // tokens per CTA of a U split
 constexpr int kDbCols = 64;  // rank columns per pass of a dB CTA
 constexpr int kSmemLoraBwd = (kLoraThreads / 32) * kUTok * 256 > 32 * kDbCols + kLoraThreads * 33
                                  ? (kLoraThreads / 32) * kUTok * 256
@@ -170,63 +171,64 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_bwd_small(LoraBwdArgs a) 
     __shared__ __align__(16) float smem[kSmemLoraBwd];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-    if ((int)blockIdx.x < a.US) {
-        // ---- U split b: rows n in [n0, n1); lane group c owns rank columns 8c .. 8c + 7
+    if ((int)blockIdx.x < a.u_ctas) {
+        // ---- U split b of four tokens: rows n in [n0, n1); lane group c owns rank columns 8c .. 8c + 7.
+        // The token groups are CTAs of their own: one after another, each waited for memory anew (16
+        // tokens, 4096 rows: 11 us for the launch)
         float(*s_red)[kUTok][256] = reinterpret_cast<float(*)[kUTok][256]>(smem);
-        const int b = blockIdx.x;
+        const int b = (int)blockIdx.x % a.US;
         const int CH = a.rp / 8;
         int CHP = 1;
         while (CHP < CH) CHP <<= 1;
         const int c = tid % CHP, G = kLoraThreads / CHP;
         const int64_t n0 = (int64_t)b * a.rows_u;
         const int64_t n1 = n0 + a.rows_u < a.N ? n0 + a.rows_u : a.N;
-        for (int64_t m0 = 0; m0 < a.M; m0 += kUTok) {
-            float acc[kUTok][8];
+        const int64_t m0 = (int64_t)((int)blockIdx.x / a.US) * kUTok;
+        float acc[kUTok][8];
+#pragma unroll
+        for (int mm = 0; mm < kUTok; ++mm)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[mm][j] = 0.f;
+        if (c < CH) {
+            for (int64_t n = n0 + tid / CHP; n < n1; n += G) {
+                float bv[8];
+                load_b8(a, n, c, bv);
+#pragma unroll
+                for (int mm = 0; mm < kUTok; ++mm) {
+                    const float y = m0 + mm < a.M ? bf16lo_to_f32(a.dY[(m0 + mm) * a.N + n]) : 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[mm][j] = __fmaf_rn(y, bv[j], acc[mm][j]);
+                }
+            }
+        }
+        for (int off = CHP; off < 32; off <<= 1)
 #pragma unroll
             for (int mm = 0; mm < kUTok; ++mm)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[mm][j] = 0.f;
-            if (c < CH) {
-                for (int64_t n = n0 + tid / CHP; n < n1; n += G) {
-                    float bv[8];
-                    load_b8(a, n, c, bv);
+                for (int j = 0; j < 8; ++j) acc[mm][j] += __shfl_xor_sync(0xffffffffu, acc[mm][j], off);
+        if (lane < CHP && c < CH)
 #pragma unroll
-                    for (int mm = 0; mm < kUTok; ++mm) {
-                        const float y = m0 + mm < a.M ? bf16lo_to_f32(a.dY[(m0 + mm) * a.N + n]) : 0.f;
+            for (int mm = 0; mm < kUTok; ++mm)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) acc[mm][j] = __fmaf_rn(y, bv[j], acc[mm][j]);
-                    }
-                }
+                for (int j = 0; j < 8; ++j) s_red[warp][mm][c * 8 + j] = acc[mm][j];
+        __syncthreads();
+        for (int e = tid; e < kUTok * a.rp; e += kLoraThreads) {
+            const int mm = e / a.rp, i = e % a.rp;
+            if (m0 + mm < a.M && i < a.r) {
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < kLoraThreads / 32; ++w) v += s_red[w][mm][i];
+                a.Upart[((int64_t)b * a.M + m0 + mm) * a.rp + i] = v;
             }
-            for (int off = CHP; off < 32; off <<= 1)
-#pragma unroll
-                for (int mm = 0; mm < kUTok; ++mm)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[mm][j] += __shfl_xor_sync(0xffffffffu, acc[mm][j], off);
-            if (lane < CHP && c < CH)
-#pragma unroll
-                for (int mm = 0; mm < kUTok; ++mm)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) s_red[warp][mm][c * 8 + j] = acc[mm][j];
-            __syncthreads();
-            for (int e = tid; e < kUTok * a.rp; e += kLoraThreads) {
-                const int mm = e / a.rp, i = e % a.rp;
-                if (m0 + mm < a.M && i < a.r) {
-                    float v = 0.f;
-#pragma unroll
-                    for (int w = 0; w < kLoraThreads / 32; ++w) v += s_red[w][mm][i];
-                    a.Upart[((int64_t)b * a.M + m0 + mm) * a.rp + i] = v;
-                }
-            }
-            __syncthreads();
         }
         return;
     }
 
-    // ---- dB rows [nb, nb + 256): thread tid owns row nb + tid
+    // ---- dB rows [nb, nb + 256): thread tid owns row nb + tid; T may be the work of the kernel before
+    grid_dep_wait();
     float* s_T = smem;                                   // [M <= 32][kDbCols]
     uint32_t* s_out = reinterpret_cast<uint32_t*>(smem + 32 * kDbCols);   // [256][33] bf16 pairs
-    const int64_t nb = (int64_t)(blockIdx.x - a.US) * kLoraThreads;
+    const int64_t nb = (int64_t)((int)blockIdx.x - a.u_ctas) * kLoraThreads;
     const int64_t n = nb + tid;
     for (int i0 = 0; i0 < a.r; i0 += kDbCols) {
         const int ic = a.r - i0 < kDbCols ? a.r - i0 : kDbCols;
