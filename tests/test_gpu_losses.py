@@ -186,6 +186,87 @@ def test_preference(M, V, P, kind, eps, margin, average, dtype):
     _run_preference(M + V + kind, M, V, P, dtype, kind, eps, margin, average)
 
 
+# more rows than the few-rows kernel takes (M, V, P, type, kind, eps, average, ld, off)
+LARGE = [(2100, 16400, 7, "bf16", 0, 0.1, False, 16400, 0), (530, 65537, 3, "bf16", 2, 0.0, True, 65537, 0),
+         (4100, 4100, 40, "fp32", 1, 0.0, False, 4103, 1), (600, 32001, 60, "bf16", 0, 0.0, True, 32010, 3)]
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("M,V,P,dtype,kind,eps,average,ld,off", LARGE)
+def test_preference_large(M, V, P, dtype, kind, eps, average, ld, off, inplace):
+    o, l, buf, _ = _run_preference(M, M, V, P, dtype, kind, eps, 0.0, average, ld=ld, off=off, beta=0.02,
+                                   inplace=inplace)
+    if not inplace:
+        again, _, _, _ = _run_preference(M, M, V, P, dtype, kind, eps, 0.0, average, ld=ld, off=off, beta=0.02)
+        assert torch.equal(o.dlogits, again.dlogits) and torch.equal(o.loss, again.loss)
+        assert torch.equal(o.rewards, again.rewards) and torch.equal(o.logp, again.logp)
+    assert ops.qlora_device_status() == 0
+
+
+def test_preference_large_agrees_with_small_calls():
+    """Pairs of 1 to 700 rows, rows in no pair before, and masked rows among them, in one large call, against one
+    small call for each pair (its gradient there is P times as large)."""
+    V, rng = 16384, np.random.default_rng(3)
+    cu = np.array([5, 6, 7, 300, 302, 700, 1400, 1400, 1401, 2100, 2500], np.int32)
+    P, M = 5, 2520
+    l = (torch.randn((M, V), device="cuda") * 3).bfloat16()
+    low = torch.finfo(torch.bfloat16).min
+    y = torch.from_numpy(rng.integers(0, V, M)).cuda()
+    y[::9] = -100
+    l[10] = low                                                 # uniform
+    l[11, 7:] = -float("inf")
+    y[11] = 3
+    l[301, 5:900] = low
+    l[400] = float("nan")
+    y[400] = -1
+    ref = torch.from_numpy(rng.standard_normal(M).astype(np.float32) - 9).cuda()
+    o = ops.preference_loss(l, y, torch.from_numpy(cu).cuda(), ref, 0.01)
+    losses = []
+    for p in range(P):
+        a, b = int(cu[2 * p]), int(cu[2 * p + 2])
+        c = torch.from_numpy(cu[2 * p:2 * p + 3] - a).cuda()
+        s = ops.preference_loss(l[a:b], y[a:b], c, ref[a:b], 0.01)
+        losses.append(s.loss.item())
+        assert torch.allclose(o.rewards[2 * p:2 * p + 2], s.rewards, rtol=1e-5, atol=0.01 * (b - a) * 2 * E_LP)
+        d = (o.dlogits[a:b].float() * P - s.dlogits.float()).abs()
+        assert (d <= 2.5 * HALF["bf16"] * s.dlogits.float().abs() + 1e-6).all()
+        assert torch.allclose(o.logp[a:b], s.logp, rtol=4 * U, atol=2 * E_LP)
+    assert abs(o.loss.item() - np.mean(losses)) <= 0.01 * 700 * 4 * E_LP
+    assert (o.dlogits[:5] == 0).all() and (o.dlogits[2500:] == 0).all() and (o.dlogits[400] == 0).all()
+
+
+def test_preference_large_on_two_streams_and_captured():
+    """Two calls at once, each of which fills the GPU, and a captured one: the results of one at a time."""
+    M, V = 2200, 16384
+    sets = [((torch.randn((M, V), device="cuda") * 3).bfloat16(), torch.randint(0, V, (M,), device="cuda")) for _ in range(2)]
+    cu = torch.tensor([0, 500, 900, 1500, 2150], dtype=torch.int32, device="cuda")
+
+    def call(s, **k):
+        o = ops.preference_loss(s[0], s[1], cu, None, 0.01, **k)
+        return [o.loss, o.rewards, o.logp, o.dlogits]
+
+    want = [call(s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = [call(s, stream=st) for s, st in zip(sets, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+    l, y = sets[0][0].clone(), sets[0][1].clone()
+    ws = ops.loss_workspace(M)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = call((l, y), ws=ws)
+    for s, ref in zip(sets, want):
+        l.copy_(s[0])
+        y.copy_(s[1])
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    assert ops.qlora_device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_preference_scaled_reference_free_and_unaligned(dtype):
     _run_preference(3, 50, 777, 3, dtype, 0, 0.0, 0.5, True, ld=781, off=3, tau=1.3, beta=2.0, ref_free=True)
