@@ -190,7 +190,7 @@ constexpr float kTop = 0x1p100f;
 constexpr uint32_t kBulk = 16384;                // bytes per bulk copy
 // CTAs per SM of the kernels that hold a row in registers: as many as leave a
 // thread its NV vectors and 60 registers more (without spills)
-constexpr int engine_ctas(int nt, int nv) { return 65536 / (nt * (nv <= 4 ? 72 : nv <= 8 ? 96 : nv <= 16 ? 128 : 255)); }
+constexpr int engine_ctas(int nt, int nv) { return 65536 / (nt * (nv <= 4 ? 72 : nv <= 8 ? 80 : nv <= 16 ? 128 : 255)); }
 
 __device__ __forceinline__ float round_k(float m, float c) { return rintf(fminf(fmaxf(m * c, -kTop), kTop)); }
 
@@ -436,6 +436,61 @@ __device__ __noinline__ void scalar_grad(const T* x, T* o, int V, int y, int v0,
 }
 
 // ---------------------------------------------------------------------------
+// short rows: one warp each, NV vectors a lane in registers
+// ---------------------------------------------------------------------------
+// A block's barriers, and a row's worth of latency for few vectors a thread,
+// took most of the time of short rows; a warp needs neither.
+constexpr int kWarpRowThreads = 128;             // four rows per CTA
+constexpr int kWarpRowVecs = 16;                 // longest row: 32 x 16 vectors
+
+template <typename T, int NV>
+struct WarpRow {
+    const T* x;
+    Row<T> sp;
+    uint4 v[NV];
+    float x1;                                    // the lane's element of the head or the tail, -inf: none
+    int e1;
+
+    __device__ __forceinline__ WarpRow(const T* x_, int V) : x(x_), sp(x_, V) {
+        const int lane = threadIdx.x & 31;
+        const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
+        e1 = lane < sp.head ? lane : lane >= 8 && lane < 8 + sp.tail ? V - sp.tail + lane - 8 : -1;
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+            v[u] = lane + 32 * u < sp.nv ? ld_v4(xv + lane + 32 * u)
+                                         : make_uint4(Pairs<T>::kNegInf, Pairs<T>::kNegInf, Pairs<T>::kNegInf,
+                                                      Pairs<T>::kNegInf);
+        x1 = e1 >= 0 ? El<T>::get(x[e1]) : -INFINITY;
+    }
+    __device__ __forceinline__ KS total(float c, float c_lo) const {
+        return warp_total(sum_pass<T, NV>(v, x1, c, c_lo));
+    }
+    // the careful form, from memory
+    __device__ __noinline__ static MS careful(const T* x, int V, float c) {
+        MS a{-INFINITY, 0.f};
+        for (int e = threadIdx.x & 31; e < V; e += 32) add1(a, El<T>::get(x[e]), c);
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) {
+            MS o;
+            o.m = __shfl_xor_sync(0xffffffffu, a.m, off);
+            o.s = __shfl_xor_sync(0xffffffffu, a.s, off);
+            a = merge(a, o, c);
+        }
+        return a;
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void warp_zero_row(T* o, int V) {
+    const int lane = threadIdx.x & 31;
+    const Row<T> sp(o, V);
+    uint4* ov = reinterpret_cast<uint4*>(o + sp.head);
+    for (int i = lane; i < sp.nv; i += 32) ov[i] = make_uint4(0, 0, 0, 0);
+    if (lane < sp.head) o[lane] = El<T>::put(0.f);
+    if (lane < sp.tail) o[V - 1 - lane] = El<T>::put(0.f);
+}
+
+// ---------------------------------------------------------------------------
 // log-probability of the target
 // ---------------------------------------------------------------------------
 struct RowArgs {
@@ -469,6 +524,37 @@ __device__ __forceinline__ double logp_of(float ly, MS t, float tau) {
 
 __device__ __forceinline__ bool in_range(float S) { return S > 0.f && S < INFINITY; }
 
+__device__ __forceinline__ void put_logp(const RowArgs& a, int64_t row, double lp, float2 st) {
+    a.logp[row] = (float)lp;
+    if (a.stats) {
+        a.stats[row] = st;
+        a.lpd[row] = lp;
+    }
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(kWarpRowThreads) k_token_logprob_warp(const RowArgs a) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t row = (int64_t)blockIdx.x * (kWarpRowThreads / 32) + (threadIdx.x >> 5);
+    if (row >= a.M) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t y = a.targets[row];
+    if (y < 0 || y >= a.V) {
+        if (lane == 0) put_logp(a, row, 0., make_float2(0.f, 1.f));
+        return;
+    }
+    const T* x = static_cast<const T*>(a.logits) + row * a.ld;
+    const float ly = El<T>::get(x[y]);
+    const KS t = WarpRow<T, NV>(x, a.V).total(a.c, a.c_lo);
+    if (in_range(t.s)) {
+        if (lane == 0) put_logp(a, row, logp_of(ly, t, a.c, a.c_lo), make_float2(t.k, t.s));
+    } else {
+        const MS ms = WarpRow<T, NV>::careful(x, a.V, a.c);
+        if (lane == 0) put_logp(a, row, logp_of(ly, ms, a.tau), make_float2(ref_of(ms.m), -ms.s));
+    }
+}
+
 constexpr int kUnroll = 4;
 constexpr float kSlack = 32.f;                   // how far a term's exponent may be above the sum's
 
@@ -487,13 +573,7 @@ __global__ void __launch_bounds__(kRowThreads) k_token_logprob(const RowArgs a) 
     const int64_t row = blockIdx.x / z;
     const int64_t y = a.targets[row];
     if (y < 0 || y >= a.V) {
-        if (rank == 0 && threadIdx.x == 0) {
-            a.logp[row] = 0.f;
-            if (a.stats) {
-                a.stats[row] = make_float2(0.f, 1.f);
-                a.lpd[row] = 0.;
-            }
-        }
+        if (rank == 0 && threadIdx.x == 0) put_logp(a, row, 0., make_float2(0.f, 1.f));
         return;
     }
     const T* x = static_cast<const T*>(a.logits) + row * a.ld;
@@ -553,24 +633,10 @@ __global__ void __launch_bounds__(kRowThreads) k_token_logprob(const RowArgs a) 
     if (tid == 0) sh.row.x = in_range(t.s) ? 1.f : 0.f;
     __syncthreads();
     if (sh.row.x != 0.f) {
-        if (rank == 0 && tid == 0) {
-            const double lp = logp_of(ly, t, a.c, a.c_lo);
-            a.logp[row] = (float)lp;
-            if (a.stats) {
-                a.stats[row] = make_float2(t.k, t.s);
-                a.lpd[row] = lp;
-            }
-        }
+        if (rank == 0 && tid == 0) put_logp(a, row, logp_of(ly, t, a.c, a.c_lo), make_float2(t.k, t.s));
     } else {
         const MS ms = careful_total(x, a.V, v0, v1, a.c, sh, rank, z);
-        if (rank == 0 && tid == 0) {
-            const double lp = logp_of(ly, ms, a.tau);
-            a.logp[row] = (float)lp;
-            if (a.stats) {
-                a.stats[row] = make_float2(ref_of(ms.m), -ms.s);
-                a.lpd[row] = lp;
-            }
-        }
+        if (rank == 0 && tid == 0) put_logp(a, row, logp_of(ly, ms, a.tau), make_float2(ref_of(ms.m), -ms.s));
     }
 }
 
@@ -935,15 +1001,15 @@ struct PolicyArgs {
     int* ticket;                 // 0 before the launch; null: the rows are dealt out in turn
 };
 
-// The row's loss terms (written by thread 0 of rank 0) and d loss / d logit
-// scale: what multiplies 1[v = y] - p_v.
+// The row's loss terms (written by the thread that is told to) and d loss /
+// d logit scale: what multiplies 1[v = y] - p_v.
 __device__ __forceinline__ float policy_row(const PolicyArgs& a, int row, float lp, float A, float w, float old,
-                                            float ref, uint32_t rank) {
+                                            float ref, bool put) {
     const float rho = a.old_logp ? expf(lp - old) : 1.f;
     const float free_ = rho * A, held = fminf(fmaxf(rho, a.lo), a.hi) * A;
     const bool clipped = held < free_;
     const float d = a.ref_logp ? ref - lp : 0.f, em = expm1f(d);
-    if (rank == 0 && threadIdx.x == 0) {
+    if (put) {
         const float pol = -(clipped ? held : free_), kl = em - d;
         a.logp[row] = lp;
         a.part[row] = make_float4(w * (pol + a.kl * kl), w * pol, w * kl, clipped ? w : 0.f);
@@ -1082,7 +1148,8 @@ __global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const Policy
             const KS t = engine_total(acc, sh, rank, z, parity, tick);
             auto row_loss = [&](float lp) {
                 return policy_row(a, row, lp, __shfl_sync(0xffffffffu, mt, 1), __shfl_sync(0xffffffffu, mt, 2),
-                                  __shfl_sync(0xffffffffu, mt, 3), __shfl_sync(0xffffffffu, mt, 4), rank);
+                                  __shfl_sync(0xffffffffu, mt, 3), __shfl_sync(0xffffffffu, mt, 4),
+                                  rank == 0 && tid == 0);
             };
             ly = __shfl_sync(0xffffffffu, mt, 0);
             if (tid < 32) {
@@ -1131,6 +1198,76 @@ __global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const Policy
     }
     // after an expired wait: the copy in flight lands before the CTA leaves
     if (tid == 0 && *abort && sh.issued > 0) tc::mbar_drain(bar, (sh.issued - 1) & 1);
+}
+
+// The same for short rows, one warp each.
+template <typename T, int NV>
+__global__ void __launch_bounds__(kWarpRowThreads) k_policy_warp(const PolicyArgs a) {
+    constexpr int N = El<T>::N;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t row = (int64_t)blockIdx.x * (kWarpRowThreads / 32) + (threadIdx.x >> 5);
+    if (row >= a.M) return;
+    const int lane = threadIdx.x & 31, V = a.V;
+    const T* x = static_cast<const T*>(a.logits) + row * a.ld;
+    T* o = static_cast<T*>(a.out) + row * a.ldo;
+    const int64_t y64 = a.targets[row];
+    const float w = a.weight[row];
+    const int y = y64 >= 0 && y64 < V && w != 0.f ? (int)y64 : -1;
+    if (y < 0) {
+        if (lane == 0) {
+            a.logp[row] = 0.f;
+            a.part[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (a.out != nullptr) warp_zero_row(o, V);
+        return;
+    }
+    const float ly = El<T>::get(x[y]), A = a.adv[row];
+    const float old = a.old_logp ? a.old_logp[row] : 0.f, ref = a.ref_logp ? a.ref_logp[row] : 0.f;
+    WarpRow<T, NV> r(x, V);
+    const KS t = r.total(a.c, a.c_lo);
+    const bool careful = !in_range(t.s);
+    MS ms{0.f, 1.f};
+    float lp;
+    if (careful) {
+        ms = WarpRow<T, NV>::careful(x, V, a.c);
+        lp = (float)logp_of(ly, ms, a.tau);
+    } else {
+        lp = (fmaf(ly, a.c_lo, fmaf(ly, a.c, -t.k)) - log2f(t.s)) * kLn2;
+        lp = lp > 0.f ? 0.f : lp;
+    }
+    const float g = policy_row(a, (int)row, lp, A, w, old, ref, lane == 0);
+    if (a.out == nullptr) return;
+    const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
+    const float k = t.k, q = -g / (careful ? ms.s : t.s);
+    if (g == 0.f) {
+        warp_zero_row(o, V);
+    } else if (careful || !same) {
+        for (int e = lane; e < V; e += 32) {
+            const float l = El<T>::get(x[e]);
+            const float p = ex2(careful ? (l - ref_of(ms.m)) * a.c : fmaf(l, a.c, -k));
+            o[e] = El<T>::put(e == y ? fmaf(q, p, g) : q * p);
+        }
+    } else {
+        const f32x2 c2 = pk2(a.c, a.c), k2 = pk2(-k, -k), q2 = pk2(q, q);
+        uint4* ov = reinterpret_cast<uint4*>(o + r.sp.head);
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            asm volatile("" : "+r"(r.v[u].x), "+r"(r.v[u].y), "+r"(r.v[u].z), "+r"(r.v[u].w));
+            float f[N];
+#pragma unroll
+            for (int j = 0; j < Pairs<T>::N; ++j) {
+                float t0, t1;
+                un2(fma2(Pairs<T>::get(r.v[u], j), c2, k2), t0, t1);
+                un2(mul2(pk2(ex2(t0), ex2(t1)), q2), f[2 * j], f[2 * j + 1]);
+            }
+            if (lane + 32 * u < r.sp.nv) ov[lane + 32 * u] = El<T>::pack(f);
+        }
+        if (r.e1 >= 0) o[r.e1] = El<T>::put(q * ex2(fmaf(r.x1, a.c, -k)));
+        const int yv = y - r.sp.head;
+        const bool mine = yv >= 0 && yv < r.sp.nv * N ? ((yv / N) & 31) == lane : r.e1 == y;
+        if (mine) o[y] = El<T>::put(fmaf(q, ex2(fmaf(ly, a.c, -k)), g));
+    }
 }
 
 constexpr int kFinishThreads = 1024;

@@ -1096,7 +1096,17 @@ int launch_rows(void (*kern)(KArg), int64_t rows, int z, int threads, cudaStream
     return e == cudaSuccess ? QLORA_OK : QLORA_ERR_LAUNCH;
 }
 
-int row_threads(int64_t nv) { return nv <= 128 ? 128 : nv <= 1024 ? 256 : loss::kRowThreads; }
+// Threads that share a row of nv vectors: the small block keeps more rows in
+// flight (16777 x 32000 bf16: 170 us with 256 threads, 164 with 128; 4185 x
+// 128256: 162 against 165), and a warp alone takes rows of up to 16 vectors a
+// lane (65536 x 2000 bf16: 125 us with 128 threads, WARP_US with a warp).
+int row_threads(int64_t nv) { return nv <= 4096 ? 128 : 256; }
+
+constexpr int kWarpRow = 32 * loss::kWarpRowVecs;    // longest row in vectors that a warp takes
+
+// kern<T, NV> for the smallest NV of 2, 4, 8, 16 vectors a lane that hold nv.
+#define QLORA_WARP_KERNEL(KERN, T, nv)                                                                          \
+    ((nv) <= 64 ? KERN<T, 2> : (nv) <= 128 ? KERN<T, 4> : (nv) <= 256 ? KERN<T, 8> : KERN<T, 16>)
 
 int launch_logprob(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float tau, const int64_t* targets,
                    float* logp, float2* stats, double* lpd, int sms, cudaStream_t st) {
@@ -1105,6 +1115,14 @@ int launch_logprob(const void* logits, int dtype, int64_t M, int64_t V, int64_t 
     split_c(tau, &a.c, &a.c_lo);
     a.targets = targets; a.logp = logp; a.stats = stats; a.lpd = lpd;
     const int64_t nv = V * (int64_t)logit_bytes(dtype) / 16;
+    if (nv <= kWarpRow) {
+        const int64_t ctas = cdiv(M, (int64_t)loss::kWarpRowThreads / 32);
+        return dtype == QLORA_LOGITS_FP32
+                   ? launch_rows<loss::RowArgs>(QLORA_WARP_KERNEL(loss::k_token_logprob_warp, float, nv), ctas, 1,
+                                                loss::kWarpRowThreads, st, a)
+                   : launch_rows<loss::RowArgs>(QLORA_WARP_KERNEL(loss::k_token_logprob_warp, uint16_t, nv), ctas, 1,
+                                                loss::kWarpRowThreads, st, a);
+    }
     const int threads = row_threads(nv);
     // a row is split over a cluster while the rows alone would not fill the SMs
     int z = 1;
@@ -1138,7 +1156,10 @@ int launch_policy_nv(loss::PolicyArgs a, int z, int sms, cudaStream_t st) {
 template <typename T>
 int launch_policy(const loss::PolicyArgs& a, int sms, cudaStream_t st) {
     const int nv = a.V * (int)sizeof(T) / 16;
-    if (nv <= 128) return launch_policy_nv<T, 128, 1>(a, 1, sms, st);
+    if (nv <= kWarpRow)
+        return launch_rows<loss::PolicyArgs>(QLORA_WARP_KERNEL(loss::k_policy_warp, T, nv),
+                                             cdiv(a.M, (int64_t)loss::kWarpRowThreads / 32), 1, loss::kWarpRowThreads,
+                                             st, a);
     int z = 1;
     while (z < loss::kMaxZ && (nv > z * 256 * 16 || (a.M * z * 2 <= 2 * (int64_t)sms && nv >= 2 * z * 256))) z *= 2;
     const int per = (nv + z - 1) / z;
