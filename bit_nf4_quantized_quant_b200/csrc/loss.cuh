@@ -347,7 +347,7 @@ template <typename T, int NT, int NV>
 __device__ __forceinline__ void grad_pass(uint4 (&v)[NV], float x1, float ly, T* o, const Row<T>& sp, int v0, int nv,
                                           int e1, int y, float c, float k, float q, float g) {
     constexpr int N = El<T>::N;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x & (NT - 1);
     const f32x2 c2 = pk2(c, c), k2 = pk2(-k, -k), q2 = pk2(q, q);
     uint4* ov = reinterpret_cast<uint4*>(o + sp.head + v0 * N);
 #pragma unroll
@@ -436,39 +436,49 @@ __device__ __noinline__ void scalar_grad(const T* x, T* o, int V, int y, int v0,
 }
 
 // ---------------------------------------------------------------------------
-// short rows: one warp each, NV vectors a lane in registers
+// short rows: one warp or one small block each, NV vectors a thread in registers
 // ---------------------------------------------------------------------------
-// A block's barriers, and a row's worth of latency for few vectors a thread,
-// took most of the time of short rows; a warp needs neither.
-constexpr int kWarpRowThreads = 128;             // four rows per CTA
-constexpr int kWarpRowVecs = 16;                 // longest row: 32 x 16 vectors
+// For few vectors a thread, the barriers of a large block and a row's latency
+// took most of the time.  Rows of up to 32 x 16 vectors take a warp, without
+// any barrier, rows of up to 128 x 16 a block of 128 threads; as many of them
+// are in flight as the registers hold, and the hardware deals them out.
+constexpr int kShortThreads = 128;
 
-template <typename T, int NV>
-struct WarpRow {
+struct ShortShared {
+    KS warp[kShortThreads / 32];
+    MS careful[kShortThreads / 32];
+};
+
+template <typename T, int NT, int NV>
+struct ShortRow {
     const T* x;
     Row<T> sp;
     uint4 v[NV];
-    float x1;                                    // the lane's element of the head or the tail, -inf: none
-    int e1;
+    float x1;                                    // the thread's element of the head or the tail, -inf: none
+    int e1, id;
 
-    __device__ __forceinline__ WarpRow(const T* x_, int V) : x(x_), sp(x_, V) {
-        const int lane = threadIdx.x & 31;
+    __device__ __forceinline__ ShortRow(const T* x_, int V) : x(x_), sp(x_, V), id(threadIdx.x & (NT - 1)) {
         const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
-        e1 = lane < sp.head ? lane : lane >= 8 && lane < 8 + sp.tail ? V - sp.tail + lane - 8 : -1;
+        e1 = id < sp.head ? id : id >= 8 && id < 8 + sp.tail ? V - sp.tail + id - 8 : -1;
 #pragma unroll
         for (int u = 0; u < NV; ++u)
-            v[u] = lane + 32 * u < sp.nv ? ld_v4(xv + lane + 32 * u)
-                                         : make_uint4(Pairs<T>::kNegInf, Pairs<T>::kNegInf, Pairs<T>::kNegInf,
-                                                      Pairs<T>::kNegInf);
+            v[u] = id + NT * u < sp.nv ? ld_v4(xv + id + NT * u)
+                                       : make_uint4(Pairs<T>::kNegInf, Pairs<T>::kNegInf, Pairs<T>::kNegInf,
+                                                    Pairs<T>::kNegInf);
         x1 = e1 >= 0 ? El<T>::get(x[e1]) : -INFINITY;
     }
-    __device__ __forceinline__ KS total(float c, float c_lo) const {
-        return warp_total(sum_pass<T, NV>(v, x1, c, c_lo));
+    __device__ __forceinline__ KS total(float c, float c_lo, ShortShared& sh) const {
+        KS t = warp_total(sum_pass<T, NV>(v, x1, c, c_lo));
+        if (NT == 32) return t;
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) sh.warp[threadIdx.x >> 5] = t;
+        __syncthreads();
+        return warp_total(lane < NT / 32 ? sh.warp[lane] : KS{-kTop, 0.f});
     }
     // the careful form, from memory
-    __device__ __noinline__ static MS careful(const T* x, int V, float c) {
+    __device__ __noinline__ static MS careful(const T* x, int V, float c, ShortShared& sh) {
         MS a{-INFINITY, 0.f};
-        for (int e = threadIdx.x & 31; e < V; e += 32) add1(a, El<T>::get(x[e]), c);
+        for (int e = threadIdx.x & (NT - 1); e < V; e += NT) add1(a, El<T>::get(x[e]), c);
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) {
             MS o;
@@ -476,18 +486,23 @@ struct WarpRow {
             o.s = __shfl_xor_sync(0xffffffffu, a.s, off);
             a = merge(a, o, c);
         }
+        if (NT == 32) return a;
+        if ((threadIdx.x & 31) == 0) sh.careful[threadIdx.x >> 5] = a;
+        __syncthreads();
+        a = sh.careful[0];
+        for (int w = 1; w < NT / 32; ++w) a = merge(a, sh.careful[w], c);
         return a;
     }
 };
 
-template <typename T>
-__device__ __forceinline__ void warp_zero_row(T* o, int V) {
-    const int lane = threadIdx.x & 31;
+template <typename T, int NT>
+__device__ __forceinline__ void zero_short_row(T* o, int V) {
+    const int id = threadIdx.x & (NT - 1);
     const Row<T> sp(o, V);
     uint4* ov = reinterpret_cast<uint4*>(o + sp.head);
-    for (int i = lane; i < sp.nv; i += 32) ov[i] = make_uint4(0, 0, 0, 0);
-    if (lane < sp.head) o[lane] = El<T>::put(0.f);
-    if (lane < sp.tail) o[V - 1 - lane] = El<T>::put(0.f);
+    for (int i = id; i < sp.nv; i += NT) ov[i] = make_uint4(0, 0, 0, 0);
+    if (id < sp.head) o[id] = El<T>::put(0.f);
+    if (id < sp.tail) o[V - 1 - id] = El<T>::put(0.f);
 }
 
 // ---------------------------------------------------------------------------
@@ -532,26 +547,27 @@ __device__ __forceinline__ void put_logp(const RowArgs& a, int64_t row, double l
     }
 }
 
-template <typename T, int NV>
-__global__ void __launch_bounds__(kWarpRowThreads) k_token_logprob_warp(const RowArgs a) {
+template <typename T, int NT, int NV>
+__global__ void __launch_bounds__(kShortThreads) k_token_logprob_short(const RowArgs a) {
+    __shared__ ShortShared sh;
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t row = (int64_t)blockIdx.x * (kWarpRowThreads / 32) + (threadIdx.x >> 5);
+    const int64_t row = (int64_t)blockIdx.x * (kShortThreads / NT) + threadIdx.x / NT;
     if (row >= a.M) return;
-    const int lane = threadIdx.x & 31;
+    const bool first = (threadIdx.x & (NT - 1)) == 0;
     const int64_t y = a.targets[row];
     if (y < 0 || y >= a.V) {
-        if (lane == 0) put_logp(a, row, 0., make_float2(0.f, 1.f));
+        if (first) put_logp(a, row, 0., make_float2(0.f, 1.f));
         return;
     }
     const T* x = static_cast<const T*>(a.logits) + row * a.ld;
     const float ly = El<T>::get(x[y]);
-    const KS t = WarpRow<T, NV>(x, a.V).total(a.c, a.c_lo);
+    const KS t = ShortRow<T, NT, NV>(x, a.V).total(a.c, a.c_lo, sh);
     if (in_range(t.s)) {
-        if (lane == 0) put_logp(a, row, logp_of(ly, t, a.c, a.c_lo), make_float2(t.k, t.s));
+        if (first) put_logp(a, row, logp_of(ly, t, a.c, a.c_lo), make_float2(t.k, t.s));
     } else {
-        const MS ms = WarpRow<T, NV>::careful(x, a.V, a.c);
-        if (lane == 0) put_logp(a, row, logp_of(ly, ms, a.tau), make_float2(ref_of(ms.m), -ms.s));
+        const MS ms = ShortRow<T, NT, NV>::careful(x, a.V, a.c, sh);
+        if (first) put_logp(a, row, logp_of(ly, ms, a.tau), make_float2(ref_of(ms.m), -ms.s));
     }
 }
 
@@ -1200,73 +1216,56 @@ __global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const Policy
     if (tid == 0 && *abort && sh.issued > 0) tc::mbar_drain(bar, (sh.issued - 1) & 1);
 }
 
-// The same for short rows, one warp each.
-template <typename T, int NV>
-__global__ void __launch_bounds__(kWarpRowThreads) k_policy_warp(const PolicyArgs a) {
-    constexpr int N = El<T>::N;
+// The same for short rows.
+template <typename T, int NT, int NV>
+__global__ void __launch_bounds__(kShortThreads) k_policy_short(const PolicyArgs a) {
+    __shared__ ShortShared sh;
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t row = (int64_t)blockIdx.x * (kWarpRowThreads / 32) + (threadIdx.x >> 5);
+    const int64_t row = (int64_t)blockIdx.x * (kShortThreads / NT) + threadIdx.x / NT;
     if (row >= a.M) return;
-    const int lane = threadIdx.x & 31, V = a.V;
+    const int id = threadIdx.x & (NT - 1), V = a.V;
     const T* x = static_cast<const T*>(a.logits) + row * a.ld;
     T* o = static_cast<T*>(a.out) + row * a.ldo;
     const int64_t y64 = a.targets[row];
     const float w = a.weight[row];
     const int y = y64 >= 0 && y64 < V && w != 0.f ? (int)y64 : -1;
     if (y < 0) {
-        if (lane == 0) {
+        if (id == 0) {
             a.logp[row] = 0.f;
             a.part[row] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (a.out != nullptr) warp_zero_row(o, V);
+        if (a.out != nullptr) zero_short_row<T, NT>(o, V);
         return;
     }
     const float ly = El<T>::get(x[y]), A = a.adv[row];
     const float old = a.old_logp ? a.old_logp[row] : 0.f, ref = a.ref_logp ? a.ref_logp[row] : 0.f;
-    WarpRow<T, NV> r(x, V);
-    const KS t = r.total(a.c, a.c_lo);
+    ShortRow<T, NT, NV> r(x, V);
+    const KS t = r.total(a.c, a.c_lo, sh);
     const bool careful = !in_range(t.s);
     MS ms{0.f, 1.f};
     float lp;
     if (careful) {
-        ms = WarpRow<T, NV>::careful(x, V, a.c);
+        ms = ShortRow<T, NT, NV>::careful(x, V, a.c, sh);
         lp = (float)logp_of(ly, ms, a.tau);
     } else {
         lp = (fmaf(ly, a.c_lo, fmaf(ly, a.c, -t.k)) - log2f(t.s)) * kLn2;
         lp = lp > 0.f ? 0.f : lp;
     }
-    const float g = policy_row(a, (int)row, lp, A, w, old, ref, lane == 0);
+    const float g = policy_row(a, (int)row, lp, A, w, old, ref, id == 0);
     if (a.out == nullptr) return;
     const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
     const float k = t.k, q = -g / (careful ? ms.s : t.s);
     if (g == 0.f) {
-        warp_zero_row(o, V);
+        zero_short_row<T, NT>(o, V);
     } else if (careful || !same) {
-        for (int e = lane; e < V; e += 32) {
+        for (int e = id; e < V; e += NT) {
             const float l = El<T>::get(x[e]);
             const float p = ex2(careful ? (l - ref_of(ms.m)) * a.c : fmaf(l, a.c, -k));
             o[e] = El<T>::put(e == y ? fmaf(q, p, g) : q * p);
         }
     } else {
-        const f32x2 c2 = pk2(a.c, a.c), k2 = pk2(-k, -k), q2 = pk2(q, q);
-        uint4* ov = reinterpret_cast<uint4*>(o + r.sp.head);
-#pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            asm volatile("" : "+r"(r.v[u].x), "+r"(r.v[u].y), "+r"(r.v[u].z), "+r"(r.v[u].w));
-            float f[N];
-#pragma unroll
-            for (int j = 0; j < Pairs<T>::N; ++j) {
-                float t0, t1;
-                un2(fma2(Pairs<T>::get(r.v[u], j), c2, k2), t0, t1);
-                un2(mul2(pk2(ex2(t0), ex2(t1)), q2), f[2 * j], f[2 * j + 1]);
-            }
-            if (lane + 32 * u < r.sp.nv) ov[lane + 32 * u] = El<T>::pack(f);
-        }
-        if (r.e1 >= 0) o[r.e1] = El<T>::put(q * ex2(fmaf(r.x1, a.c, -k)));
-        const int yv = y - r.sp.head;
-        const bool mine = yv >= 0 && yv < r.sp.nv * N ? ((yv / N) & 31) == lane : r.e1 == y;
-        if (mine) o[y] = El<T>::put(fmaf(q, ex2(fmaf(ly, a.c, -k)), g));
+        grad_pass<T, NT, NV>(r.v, r.x1, ly, o, r.sp, 0, r.sp.nv, r.e1, y, a.c, k, q, g);
     }
 }
 

@@ -1102,11 +1102,15 @@ int launch_rows(void (*kern)(KArg), int64_t rows, int z, int threads, cudaStream
 // lane (65536 x 2000 bf16: 125 us with 128 threads, WARP_US with a warp).
 int row_threads(int64_t nv) { return nv <= 4096 ? 128 : 256; }
 
-constexpr int kWarpRow = 32 * loss::kWarpRowVecs;    // longest row in vectors that a warp takes
+// Longest rows in vectors that a warp, a block of 128 threads takes in registers.
+constexpr int kWarpRow = 32 * 16, kBlockRow = 128 * 16;
 
-// kern<T, NV> for the smallest NV of 2, 4, 8, 16 vectors a lane that hold nv.
-#define QLORA_WARP_KERNEL(KERN, T, nv)                                                                          \
-    ((nv) <= 64 ? KERN<T, 2> : (nv) <= 128 ? KERN<T, 4> : (nv) <= 256 ? KERN<T, 8> : KERN<T, 16>)
+int64_t short_ctas(int64_t M, int nv) { return nv <= kWarpRow ? cdiv(M, (int64_t)loss::kShortThreads / 32) : M; }
+
+// The kernel for a short row of nv vectors: 2, 4, 8, 16 vectors a lane, then 8, 16 a thread.
+#define QLORA_SHORT_KERNEL(KERN, T, nv)                                                                  \
+    ((nv) <= 64 ? KERN<T, 32, 2> : (nv) <= 128 ? KERN<T, 32, 4> : (nv) <= 256 ? KERN<T, 32, 8>           \
+     : (nv) <= 512 ? KERN<T, 32, 16> : (nv) <= 1024 ? KERN<T, 128, 8> : KERN<T, 128, 16>)
 
 int launch_logprob(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float tau, const int64_t* targets,
                    float* logp, float2* stats, double* lpd, int sms, cudaStream_t st) {
@@ -1115,17 +1119,18 @@ int launch_logprob(const void* logits, int dtype, int64_t M, int64_t V, int64_t 
     split_c(tau, &a.c, &a.c_lo);
     a.targets = targets; a.logp = logp; a.stats = stats; a.lpd = lpd;
     const int64_t nv = V * (int64_t)logit_bytes(dtype) / 16;
-    if (nv <= kWarpRow) {
-        const int64_t ctas = cdiv(M, (int64_t)loss::kWarpRowThreads / 32);
+    int z = 1;
+    // with few rows a row is better split over a cluster than left to one small block
+    if (nv <= kWarpRow || (nv <= kBlockRow && 2 * M > 4 * (int64_t)sms)) {
+        const int64_t ctas = short_ctas(M, (int)nv);
         return dtype == QLORA_LOGITS_FP32
-                   ? launch_rows<loss::RowArgs>(QLORA_WARP_KERNEL(loss::k_token_logprob_warp, float, nv), ctas, 1,
-                                                loss::kWarpRowThreads, st, a)
-                   : launch_rows<loss::RowArgs>(QLORA_WARP_KERNEL(loss::k_token_logprob_warp, uint16_t, nv), ctas, 1,
-                                                loss::kWarpRowThreads, st, a);
+                   ? launch_rows<loss::RowArgs>(QLORA_SHORT_KERNEL(loss::k_token_logprob_short, float, nv), ctas, 1,
+                                                loss::kShortThreads, st, a)
+                   : launch_rows<loss::RowArgs>(QLORA_SHORT_KERNEL(loss::k_token_logprob_short, uint16_t, nv), ctas, 1,
+                                                loss::kShortThreads, st, a);
     }
     const int threads = row_threads(nv);
     // a row is split over a cluster while the rows alone would not fill the SMs
-    int z = 1;
     while (z < loss::kMaxZ && M * z * 2 <= 4 * (int64_t)sms && nv >= 2 * z * threads) z *= 2;
     return dtype == QLORA_LOGITS_FP32 ? launch_rows<loss::RowArgs>(loss::k_token_logprob<float>, M, z, threads, st, a)
                                       : launch_rows<loss::RowArgs>(loss::k_token_logprob<uint16_t>, M, z, threads, st, a);
@@ -1156,10 +1161,9 @@ int launch_policy_nv(loss::PolicyArgs a, int z, int sms, cudaStream_t st) {
 template <typename T>
 int launch_policy(const loss::PolicyArgs& a, int sms, cudaStream_t st) {
     const int nv = a.V * (int)sizeof(T) / 16;
-    if (nv <= kWarpRow)
-        return launch_rows<loss::PolicyArgs>(QLORA_WARP_KERNEL(loss::k_policy_warp, T, nv),
-                                             cdiv(a.M, (int64_t)loss::kWarpRowThreads / 32), 1, loss::kWarpRowThreads,
-                                             st, a);
+    if (nv <= kWarpRow || (nv <= kBlockRow && 2 * a.M > 4 * (int64_t)sms))
+        return launch_rows<loss::PolicyArgs>(QLORA_SHORT_KERNEL(loss::k_policy_short, T, nv), short_ctas(a.M, nv), 1,
+                                             loss::kShortThreads, st, a);
     int z = 1;
     while (z < loss::kMaxZ && (nv > z * 256 * 16 || (a.M * z * 2 <= 2 * (int64_t)sms && nv >= 2 * z * 256))) z *= 2;
     const int per = (nv + z - 1) / z;
