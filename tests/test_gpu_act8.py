@@ -128,6 +128,21 @@ def test_bwd_equals_the_backward_of_the_restored_tensor(M, N, K, r, fmt):
     assert ops.qlora_device_status() == 0
 
 
+@pytest.mark.parametrize("M", [17, 70, 200])
+def test_bwd_dropout_without_T_and_fp4(M):
+    """T recomputed from the dropped checkpoint, and an FP4 weight."""
+    _, X, A, B, dY = _layer(M, 200, 320, 24, M)
+    w = ops.quant4_quantize_dq(inputs.weight(9, 0, 200, 320, 0.02).cuda(), ops.QLORA_QUANT_FP4)
+    for fmt in FMTS:
+        x8 = ops.act8_quantize(X, fmt)
+        Xr = ops.act8_dequant(x8)
+        got = ops.qlora_linear_bwd_act8(x8, dY, w, A, B, 1.5, dropout_p=0.3, seed=11, offset=2)
+        want = ops.qlora_linear_bwd_dropout(Xr, dY, w, A, B, 1.5, 0.3, 11, 2)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        got = ops.qlora_linear_bwd_act8(x8, dY, w, A, B, 1.5)
+        assert all(torch.equal(a, b) for a, b in zip(got, ops.qlora_linear_bwd(Xr, dY, w, A, B, 1.5)))
+
+
 @pytest.mark.parametrize("M", [24, 160])
 def test_bwd_against_the_formula(oracle_mod, M):
     """dA and dB against fp64 products of the checkpoint's values (the tolerance of the layer's own parity tests:

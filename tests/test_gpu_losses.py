@@ -82,14 +82,13 @@ def test_logprob_rows_at_any_alignment(ld, off, dtype):
     _check_logp(ops.token_logprob(l, y), l64, yn, 1.0)
 
 
-def _masked_rows(dtype):
+def _masked_rows(dtype, V):
     """Rows with -inf entries, of the type's lowest value, of one finite entry, without any; a target at -inf; NaN
-    and +inf rows; rows out of play that hold NaN."""
-    low = torch.finfo(DT[dtype]).min
+    and +inf rows; rows out of play that hold NaN; values beyond 2^100 on both sides."""
+    low, big = torch.finfo(DT[dtype]).min, 2.0 ** 110
     inf = float("inf")
-    V = 300
-    l = torch.from_numpy(np.random.default_rng(4).standard_normal((10, V)).astype(np.float32)).to(DT[dtype])
-    y = np.array([5, 5, 5, 5, 5, 5, 5, -100, V + 3, 5])
+    l = torch.from_numpy(np.random.default_rng(4).standard_normal((12, V)).astype(np.float32)).to(DT[dtype])
+    y = np.array([5, 5, 5, 5, 5, 5, 5, -100, V + 3, 5, 5, 5])
     l[0, 6:] = -inf
     l[1] = low
     l[2] = -inf
@@ -101,30 +100,66 @@ def _masked_rows(dtype):
     l[7] = float("nan")
     l[8] = inf
     l[9, 10:200] = low
-    return l.cuda(), torch.from_numpy(y).cuda(), y, V
+    l[10] = -big
+    l[10, ::2] = -2 * big                                       # only entries beyond the range: half of them lead
+    l[11] = 1.0
+    l[11, 5] = big
+    return l.cuda(), torch.from_numpy(y).cuda(), y
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-def test_masked_rows(dtype):
-    l, y, yn, V = _masked_rows(dtype)
+@pytest.mark.parametrize("V", [300, 5000, 40000])
+def test_masked_rows(V, dtype):
+    l, y, yn = _masked_rows(dtype, V)
+    M = len(yn)
     lp = ops.token_logprob(l, y).cpu().numpy().astype(np.float64)
     l64 = l.double().cpu().numpy()
     ref, ls, live = tr.token_logprob(l64, yn)
     assert np.isnan(lp[[3, 5, 6]]).all() and np.isnan(ref[[3, 5, 6]]).all()
     # (row 2, one finite entry: 0 within E_LP like any other, by the check below, and never above 0)
     assert lp[4] == -np.inf and lp[2] <= 0 and lp[7] == 0 and lp[8] == 0
+    assert abs(lp[10] + np.log(V // 2)) <= E_LP and abs(lp[11]) <= E_LP     # 5 is one of row 10's V / 2 leaders
     assert abs(lp[1] + np.log(V)) <= E_LP
-    ok = [0, 1, 2, 9]
+    ok = [0, 1, 2, 9, 10, 11]
     assert (np.abs(lp[ok] - ref[ok]) <= E_LP + 4 * U * np.abs(ref[ok])).all()
-    # gradients of a policy loss with ratio 1 and advantage -1: weight d / d logp = +1 per row
-    ones, w = torch.ones(10, device="cuda"), torch.ones(10, device="cuda")
-    out = ops.policy_loss(l, y, -ones, w, None, None)
+    # the gradient of a sum of log-probabilities, by a policy loss with ratio 1 and advantage -1
+    ones = torch.ones(M, device="cuda")
+    out = ops.policy_loss(l, y, -ones, ones, None, None)
+    # and by the chosen sequences of an IPO loss: d loss / d delta = 2 (delta - 1 / (2 beta)), one pair a row
+    for r in (0, 1, 2, 4, 9, 10, 11):
+        want = np.exp(ls[r])
+        want = np.where(np.arange(V) == yn[r], 1.0, 0.0) - want
+        grads = [out.dlogits[r]]
+        if r != 4:
+            cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+            pair = torch.stack([l[r], l[0]])
+            o = ops.preference_loss(pair, y[[r, 7]], cu, None, 0.5, kind=ops.QLORA_PREF_IPO)
+            grads.append(o.dlogits[0].float() / (2 * (ref[r] - 1.0)))
+        for g in grads:
+            # the second gradient was divided by a factor that is off by 2 E_LP of 2 or more, and rounded before that
+            lim = np.exp(ls[r]) * 6e-5 + (HALF[dtype] + 2 * E_LP) * np.abs(want) + 2.0 ** -126
+            assert (np.abs(g.double().cpu().numpy() - want) <= lim).all(), r
     g = out.dlogits.double().cpu().numpy()
     assert np.isnan(g[[3, 5, 6]]).all() and (g[[7, 8]] == 0).all()
-    want = tr.dlogits(ls, yn, live, np.ones(10), 1.0)
-    for r in (0, 1, 2, 4, 9):
-        lim = np.exp(ls[r]) * 6e-5 + HALF[dtype] * np.abs(want[r]) + 2.0 ** -126
-        assert (np.abs(g[r] - want[r]) <= lim).all(), r
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,V", [(1500, 700), (1400, 5003), (1300, 20001), (700, 40003)])
+def test_in_place_equals_out_of_place(M, V, dtype):
+    """Many rows of every kernel's width: the gradient over the logits, bit for bit the one written elsewhere."""
+    l = (torch.randn((M, V), device="cuda") * 3).to(DT[dtype])
+    y = torch.randint(0, V, (M,), device="cuda")
+    y[::5] = -100
+    w = torch.rand(M, device="cuda")
+    w[1::7] = 0
+    cu = torch.linspace(0, M - 3, 21, device="cuda").int()
+    for f in (lambda t, **k: ops.policy_loss(t, y, w - 0.5, w, None, None, **k),
+              lambda t, **k: ops.preference_loss(t, y, cu, None, 0.01, **k)):
+        a = f(l)
+        t = l.clone()
+        b = f(t, dlogits=t)
+        assert torch.equal(a.dlogits, b.dlogits) and torch.equal(a.logp, b.logp)
+        assert torch.isfinite(a.dlogits).all() and (a.dlogits[::5] == 0).all()
 
 
 # ------------------------------------------------------------------ preference
@@ -384,7 +419,7 @@ def test_policy(M, V, dtype):
     _run_policy(M + V, M, V, dtype)
 
 
-@pytest.mark.parametrize("V", [40, 2100, 9000, 40000])
+@pytest.mark.parametrize("V", [40, 2100, 9000, 20000, 40000])
 def test_policy_every_row_is_taken_once(V):
     """Row counts around what the GPU holds at once, and dozens of times that: every row's log-probability and
     gradient row are those of the row alone."""
