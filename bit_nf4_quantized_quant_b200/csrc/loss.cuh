@@ -275,39 +275,67 @@ struct EngineShared {
     int tick[2];                                 // the row after the next two, by row parity
     float edge[16];                              // the row's head and tail elements
     int issued;                                  // copies started
-    unsigned long long bar;
+    unsigned long long bar;                      // the row's copy
+    unsigned long long xbar[2];                  // what the cluster's CTAs send, by row parity
     int abort;
 };
 
-// Rank 0's warp 0 leaves the ticket in every CTA of the cluster (to be read
-// behind the next barrier).
-__device__ __forceinline__ void share_tick(EngineShared& sh, uint32_t rank, uint32_t z, int parity, int tick) {
-    if (rank != 0 || threadIdx.x >= 32) return;
+// What the CTAs of a cluster tell one another about a row: every CTA sends its
+// (k, s) to all of them, and rank 0 the ticket, by asynchronous stores that
+// complete on the receiver's barrier of the row's parity.  One warp sends and
+// waits; the block learns of it at its next barrier.  (A cluster barrier of all
+// threads in its place took ~1 us more per row.)  Two parities are enough: a CTA
+// sends for a row only after it has received all of the row before.
+__device__ __forceinline__ void engine_init(EngineShared& sh) {
+    if (threadIdx.x == 0) {
+        sh.abort = 0;
+        sh.issued = 0;
+        tc::mbar_init(smem_u32(&sh.bar), 1);
+        tc::mbar_init(smem_u32(&sh.xbar[0]), 1);
+        tc::mbar_init(smem_u32(&sh.xbar[1]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+}
+
+// Warp 0 of every CTA: (k, s) of all ranks added up; the ticket is in
+// sh.tick[row & 1] behind the block's next barrier.  `row` counts the rows of
+// this cluster from 0.
+__device__ __forceinline__ KS engine_exchange(KS v, EngineShared& sh, uint32_t rank, uint32_t z, uint32_t row,
+                                              int tick) {
+    const int lane = threadIdx.x & 31, parity = row & 1;
     tick = __shfl_sync(0xffffffffu, tick, 0);
-    if (threadIdx.x < z) {
-        const uint32_t at = smem_u32(&sh.tick[parity]);
-        if (z == 1) asm volatile("st.shared.s32 [%0], %1;" ::"r"(at), "r"(tick) : "memory");
-        else asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(mapa(at, threadIdx.x)), "r"(tick) : "memory");
+    if (z == 1) {
+        if (lane == 0) sh.tick[parity] = tick;
+        return v;
+    }
+    const uint32_t xb = smem_u32(&sh.xbar[parity]);
+    if (lane == 0) tc::mbar_expect_tx(xb, z * 8 + 4);
+    if (lane < (int)z) {
+        const uint32_t bar = mapa(xb, lane);
+        const unsigned long long ks = (unsigned long long)__float_as_uint(v.s) << 32 | __float_as_uint(v.k);
+        asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
+                         mapa(smem_u32(&sh.rank[parity][rank]), lane)),
+                     "l"(ks), "r"(bar)
+                     : "memory");
+        if (rank == 0)
+            asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                             mapa(smem_u32(&sh.tick[parity]), lane)),
+                         "r"(tick), "r"(bar)
+                         : "memory");
     }
     __syncwarp();
+    tc::mbar_wait(xb, (row >> 1) & 1, &sh.abort);
+    return warp_total(lane < (int)z ? sh.rank[parity][lane] : KS{-kTop, 0.f});
 }
 
 // The row's (k, s) in warp 0 of every CTA of the cluster (the other warps
-// return what they have at once): one block barrier, and one cluster barrier
-// for a row that several CTAs share.
-__device__ __forceinline__ KS engine_total(KS v, EngineShared& sh, uint32_t rank, uint32_t z, int parity, int tick) {
+// return what they have at once).
+__device__ __forceinline__ KS engine_total(KS v, EngineShared& sh, uint32_t rank, uint32_t z, uint32_t row, int tick) {
     const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     v = warp_total(v);
     if (lane == 0) sh.warp[threadIdx.x >> 5] = v;
     __syncthreads();
-    if (threadIdx.x < 32) v = warp_total(lane < nw ? sh.warp[lane] : KS{-kTop, 0.f});
-    share_tick(sh, rank, z, parity, tick);
-    if (z == 1) return v;
-    if (threadIdx.x < z) st_dsmem_f2(mapa(smem_u32(&sh.rank[parity][rank]), threadIdx.x), v.k, v.s);
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();
-    if (threadIdx.x < 32) v = warp_total(lane < (int)z ? sh.rank[parity][lane] : KS{-kTop, 0.f});
+    if (threadIdx.x < 32) v = engine_exchange(warp_total(lane < nw ? sh.warp[lane] : KS{-kTop, 0.f}), sh, rank, z, row, tick);
     return v;
 }
 
@@ -580,16 +608,15 @@ template <typename T>
 __global__ void __launch_bounds__(kRowThreads) k_token_logprob(const RowArgs a) {
     __shared__ EngineShared sh;
     const uint32_t rank = cluster_rank(), z = cluster_size();
-    if (z > 1) {
-        cluster_arrive();
-        cluster_wait();                          // every CTA of the cluster runs
-    }
+    engine_init(sh);
+    if (z > 1) cluster_arrive();
     grid_dep_wait();
     grid_dep_launch();
     const int64_t row = blockIdx.x / z;
     const int64_t y = a.targets[row];
     if (y < 0 || y >= a.V) {
         if (rank == 0 && threadIdx.x == 0) put_logp(a, row, 0., make_float2(0.f, 1.f));
+        if (z > 1) cluster_wait();
         return;
     }
     const T* x = static_cast<const T*>(a.logits) + row * a.ld;
@@ -645,6 +672,7 @@ __global__ void __launch_bounds__(kRowThreads) k_token_logprob(const RowArgs a) 
     float sa, sb;
     un2(s2, sa, sb);
     acc.s = sa + sb;
+    if (z > 1) cluster_wait();                   // every CTA of the cluster runs
     const KS t = engine_total(acc, sh, rank, z, 0, 0);
     if (tid == 0) sh.row.x = in_range(t.s) ? 1.f : 0.f;
     __syncthreads();
@@ -1053,12 +1081,7 @@ __global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const Policy
     const uint4 none = make_uint4(Pairs<T>::kNegInf, Pairs<T>::kNegInf, Pairs<T>::kNegInf, Pairs<T>::kNegInf);
 #pragma unroll
     for (int u = 0; u < NV; ++u) buf[tid + u * NT] = none;
-    if (tid == 0) {
-        sh.abort = 0;
-        sh.issued = 0;
-        tc::mbar_init(bar, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
+    engine_init(sh);
     tc::fence_proxy_async();                              // the copies into buf come after these stores
     __syncthreads();
     if (z > 1) cluster_arrive();
@@ -1068,7 +1091,8 @@ __global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const Policy
     T* o0 = static_cast<T*>(a.out);
     const int zlog = __ffs((int)z) - 1, M = (int)a.M, V = a.V, G = gridDim.x >> zlog;     // z is a power of two
 
-    int waited = 0, parity = 0;
+    int waited = 0;
+    uint32_t nth = 0;                                     // rows of this cluster so far
     // this CTA's vectors of a row, and their copy into buf (one thread)
     auto span = [&](const Row<T>& sp, int& v0, int& v1) {
         const int per = (sp.nv + (int)z - 1) >> zlog;
@@ -1161,7 +1185,7 @@ __global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const Policy
                 }
             }
             const KS acc = sum_pass<T, NV>(v, x1, a.c, a.c_lo);
-            const KS t = engine_total(acc, sh, rank, z, parity, tick);
+            const KS t = engine_total(acc, sh, rank, z, nth, tick);
             auto row_loss = [&](float lp) {
                 return policy_row(a, row, lp, __shfl_sync(0xffffffffu, mt, 1), __shfl_sync(0xffffffffu, mt, 2),
                                   __shfl_sync(0xffffffffu, mt, 3), __shfl_sync(0xffffffffu, mt, 4),
@@ -1176,7 +1200,7 @@ __global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const Policy
                 if (tid == 0) sh.row = make_float4(t.k, -g / t.s, g, fine ? 0.f : 1.f);
             }
             __syncthreads();
-            tick = sh.tick[parity];
+            tick = sh.tick[nth & 1];
             const float4 rv = sh.row;
             k = rv.x; q = rv.y; g = rv.z;
             careful = rv.w != 0.f;
@@ -1187,14 +1211,10 @@ __global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const Policy
             }
         } else {
             if (nlive && tid == 0) load(nrow);
-            share_tick(sh, rank, z, parity, tick);
-            if (z == 1) {
-                __syncthreads();
-            } else {
-                cluster_arrive();
-                cluster_wait();
-            }
-            tick = sh.tick[parity];
+            __syncthreads();                              // the ticket of the row before has been read
+            if (tid < 32) engine_exchange(KS{0.f, 0.f}, sh, rank, z, nth, tick);
+            __syncthreads();
+            tick = sh.tick[nth & 1];
             if (rank == 0 && tid == 0) {
                 a.logp[row] = 0.f;
                 a.part[row] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1208,7 +1228,7 @@ __global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const Policy
         } else {
             grad_pass<T, NT, NV>(v, x1, ly, o, sp, v0, nv, e1, y, a.c, k, q, g);
         }
-        parity ^= 1;
+        ++nth;
         y = ny;
         mt = nmt;
     }
