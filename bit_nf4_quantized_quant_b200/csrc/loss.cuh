@@ -303,11 +303,11 @@ __device__ __forceinline__ void engine_init(EngineShared& sh) {
 __device__ __forceinline__ KS engine_exchange(KS v, EngineShared& sh, uint32_t rank, uint32_t z, uint32_t row,
                                               int tick) {
     const int lane = threadIdx.x & 31, parity = row & 1;
-    tick = __shfl_sync(0xffffffffu, tick, 0);
     if (z == 1) {
-        if (lane == 0) sh.tick[parity] = tick;
+        if (lane == 0) sh.tick[parity] = tick;   // lane 0 drew it
         return v;
     }
+    tick = __shfl_sync(0xffffffffu, tick, 0);
     const uint32_t xb = smem_u32(&sh.xbar[parity]);
     if (lane == 0) tc::mbar_expect_tx(xb, z * 8 + 4);
     if (lane < (int)z) {
