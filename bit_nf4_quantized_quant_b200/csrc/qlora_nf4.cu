@@ -597,6 +597,10 @@ int launch_tc2(const nf4dq_weight* w, const uint16_t* act, int64_t M, const uint
     a.lora_w = lora_w; a.ldl = ldl; a.r = r; a.lper = (int)rup(r, 16); a.nlora = lora ? (int)cdiv(lw, 64) : 0;
     a.out = out; a.M = M; a.N = N; a.K = K; a.n_out = n_out; a.n_red = n_red;
     Tc2Sched sc = tc2_schedule(M, n_out, pairs, BWD);
+    // every pair needs a unit of its own: the owner of a tile waits for a count from each pair
+    // between the tile's first one and itself, and a pair with an empty run counts nothing
+    // (reductions of one or two steps, few tiles: whole tiles then, the split gains nothing)
+    if (sc.ntiles * (cdiv(n_red, tc2::BK) + a.nlora) < pairs) sc.sk = false;
     // the counters were zeroed by the kernel before this one (the T or U product), or below
     if (sc.sk && (sk_part_bytes(sc, pairs) > p.sk_part_bytes || sk_flag_bytes(sc) > p.sk_flag_bytes)) sc.sk = false;
     a.sk = sc.sk ? 1 : 0;

@@ -354,3 +354,40 @@ def test_fused_kernels_repeat_bit_identically(M, N, K, r, bwd):
     torch.cuda.synchronize()
     assert ops.qlora_device_status() == 0
     assert bool(same)
+
+
+@pytest.mark.parametrize("M,N,K,r", [(133, 64, 6592, 24), (458, 64, 7488, 8), (3114, 64, 448, 16),   # backward
+                                     (133, 6592, 64, 24), (458, 7488, 64, 8),                        # forward
+                                     (133, 128, 6592, 16)])                  # backward with dropout
+@pytest.mark.parametrize("p", [0.0, 0.1])
+def test_fewer_units_than_pairs(oracle_mod, M, N, K, r, p):
+    """A reduction of one or two steps over fewer tiles than SM pairs: (tile, step) units do not
+    reach every pair, so tiles are not split (an owner would wait for a pair with no work)."""
+    s = 32.0 / r
+    W, X, A, B, dY, Wd, w = _setup(oracle_mod, M, N, K, r, seed=M + N + K + r)
+    Xc, Ac, Bc, dYc = X.cuda(), A.cuda(), B.cuda(), dY.cuda()
+    X64, A64, B64, dY64 = (inputs.to_f64(t) for t in (X, A, B, dY))
+    if p:
+        keep, c = oracle_mod.dropout_mask(7, 11, M, K, p), oracle_mod.dropout_scale(p)
+        Y = ops.qlora_linear_fwd_dropout(Xc, w, Ac, Bc, s, p, 7, 11)
+        dX, dA, dB = ops.qlora_linear_bwd_dropout(Xc, dYc, w, Ac, Bc, s, p, 7, 11)
+        Yr, _ = oracle_mod.linear_fwd_dropout(X64, Wd, A64, B64, s, keep, c)
+        dXr, dAr, dBr = oracle_mod.linear_bwd_dropout(X64, dY64, Wd, A64, B64, s, keep, c)
+    else:
+        Y = ops.qlora_linear_fwd(Xc, w, Ac, Bc, s)
+        dX, dA, dB = ops.qlora_linear_bwd(Xc, dYc, w, Ac, Bc, s)
+        Yr, _ = oracle_mod.linear_fwd(X64, Wd, A64, B64, s)
+        dXr, dAr, dBr = oracle_mod.linear_bwd(X64, dY64, Wd, A64, B64, s)
+    torch.cuda.synchronize()
+    assert ops.qlora_device_status() == 0
+    _close(inputs.to_f64(Y), Yr, "Y")
+    # with dropout dX is rounded to bf16 twice: the base product dY W', and its sum with the masked
+    # LoRA term, each by at most 2^-8 of the value rounded, and the first does not shrink where the
+    # two terms cancel.  The rest is fp32: 2^-24 for each of the N products' additions.
+    base = dY64 @ Wd
+    err = np.abs(inputs.to_f64(dX) - dXr)
+    lim = 2.0 ** -8 * (np.abs(base) * (1 + 2.0 ** -8) + np.abs(dXr)) if p else 2.0 ** -8 * np.abs(dXr)
+    mags = np.abs(dY64) @ np.abs(Wd) + abs(s) * (np.abs(dY64) @ np.abs(B64)) @ np.abs(A64) * (c if p else 1.0)
+    assert (err <= lim + (N + r) * 2.0 ** -24 * mags + (0 if p else 2.0 ** -16 * mags)).all(), err.max()
+    _close(inputs.to_f64(dA), dAr, "dA")
+    _close(inputs.to_f64(dB), dBr, "dB")

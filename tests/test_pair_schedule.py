@@ -118,3 +118,24 @@ def test_bad_arguments():
     buf = (ctypes.c_int64 * 3)()
     assert ops.lib().qlora_pair_spans(10, 5, 3, 2, buf, 1) == ops.QLORA_ERR_VALUE     # pair >= npairs
     assert ops.lib().qlora_pair_spans(10, 5, 0, 2, None, 1) == ops.QLORA_ERR_NULL
+
+
+@pytest.mark.parametrize("pairs", [74, 73, 70, 64])
+@pytest.mark.parametrize("nsteps", [1, 2, 3])
+def test_short_reductions_need_a_unit_for_every_pair(pairs, nsteps):
+    """An owner waits for a count from each pair between its tile's first one and itself.  That
+    is right exactly when no pair's run is empty, which is why tiles are split only where there
+    are as many units as pairs."""
+    for ntiles in range(cdiv(pairs, 3), 2 * pairs):
+        spans = [ops.pair_spans(ntiles, nsteps, p, pairs) for p in range(pairs)]
+        if ntiles * nsteps >= pairs:
+            assert all(spans)
+        else:
+            assert not all(spans)
+            continue
+        for p, sp in enumerate(spans):
+            for (t, s0, s1) in sp:
+                if s1 == nsteps and s0 > 0:
+                    pf = _owner_first_pair(p, pairs, ntiles, nsteps, t)
+                    heads = [q for q in range(p) if any(tt == t for (tt, _, _) in spans[q])]
+                    assert heads == list(range(pf, p))
