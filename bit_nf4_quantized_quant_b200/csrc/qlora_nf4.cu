@@ -1071,6 +1071,18 @@ int check_logits(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld
     return QLORA_OK;
 }
 
+// Whether a row of the gradient overlaps a row of the logits, other than as the same row of the
+// same place: rows i and j whose distance in elements is less than V.  With equal row pitches
+// that is a matter of the offset alone; unequal ones may not share a range at all.
+bool rows_collide(const void* logits, int64_t ld, const void* grad, int64_t ldd, int64_t M, int64_t V, size_t es) {
+    const uint64_t a = reinterpret_cast<uintptr_t>(logits), b = reinterpret_cast<uintptr_t>(grad);
+    if (a == b && (ld == ldd || M == 1)) return false;
+    if (b >= a + (uint64_t)((M - 1) * ld + V) * es || a >= b + (uint64_t)((M - 1) * ldd + V) * es) return false;
+    if (ld != ldd) return true;
+    const uint64_t at = (a > b ? a - b : b - a) % ((uint64_t)ld * es);
+    return at < (uint64_t)V * es || (uint64_t)(ld - V) * es < at;
+}
+
 // The fp32 number c below tau log2 e, and the rest of it.  The rest is positive:
 // with another sign, or 0, the kernels' -inf c + -inf c_lo would be a NaN.
 void split_c(float tau, float* c, float* c_lo) {
@@ -1103,7 +1115,7 @@ int launch_rows(void (*kern)(KArg), int64_t rows, int z, int threads, cudaStream
 // Threads that share a row of nv vectors: the small block keeps more rows in
 // flight (16777 x 32000 bf16: 170 us with 256 threads, 164 with 128; 4185 x
 // 128256: 162 against 165), and a warp alone takes rows of up to 16 vectors a
-// lane (65536 x 2000 bf16: 125 us with 128 threads, WARP_US with a warp).
+// lane (65536 x 2000 bf16: 125 us with 128 threads, 47 with a warp).
 int row_threads(int64_t nv) { return nv <= 4096 ? 128 : 256; }
 
 // Longest rows in vectors that a warp, a block of 128 threads takes in registers.
@@ -1666,6 +1678,7 @@ int preference_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t
     if (!aligned_to(cu_seqlens, 4) || (ref_logp && !aligned_to(ref_logp, 4)) || !aligned_to(loss, 4) ||
         !aligned_to(rewards, 4) || !aligned_to(logp, 4) || (dlogits && !aligned_to(dlogits, logit_bytes(dtype))))
         return QLORA_ERR_ALIGN;
+    if (dlogits && rows_collide(logits, ld, dlogits, ldd, M, V, logit_bytes(dtype))) return QLORA_ERR_SHAPE;
     if (!ws) return QLORA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return QLORA_ERR_ALIGN;
     if (ws_bytes < loss_workspace_bytes(M)) return QLORA_ERR_WORKSPACE;
@@ -1720,6 +1733,7 @@ int policy_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld,
         (ref_logp && !aligned_to(ref_logp, 4)) || !aligned_to(stats, 4) || !aligned_to(logp, 4) ||
         (dlogits && !aligned_to(dlogits, logit_bytes(dtype))))
         return QLORA_ERR_ALIGN;
+    if (dlogits && rows_collide(logits, ld, dlogits, ldd, M, V, logit_bytes(dtype))) return QLORA_ERR_SHAPE;
     if (!ws) return QLORA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return QLORA_ERR_ALIGN;
     if (ws_bytes < loss_workspace_bytes(M)) return QLORA_ERR_WORKSPACE;

@@ -338,7 +338,8 @@ QLORA_API int qlora_linear_bwd_act8(const act8_tensor* X, const qlora_bf16* dY, 
  *     nothing above -inf, gives NaN.
  *   - dlogits [M, V], rows ldd apart, of the logits' type, or NULL for the
  *     loss alone; columns beyond V are not written.  It may be the logits
- *     themselves (same pointer, ldd = ld); otherwise the two must not overlap.
+ *     themselves (same pointer, ldd = ld); rows that overlap in any other way are
+ *     refused (QLORA_ERR_SHAPE).
  *     It is grad_scale times the gradient of the loss.
  *   - ws: at least loss_workspace_bytes(M) bytes, 256-byte aligned; calls that
  *     overlap on the GPU need separate ones.

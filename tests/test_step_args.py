@@ -134,6 +134,36 @@ def test_policy_refusals(lib):
     assert call(ws=None) == -5 and call(n=16) == -5 and call(ws=P(0x1010)) == -4
 
 
+@pytest.mark.parametrize("es", [2, 4])
+def test_gradient_rows_that_overlap_other_rows_are_refused(lib, es):
+    """At the logits' own place the gradient is in place; beside their rows, in the same buffer, it
+    is apart; everywhere else in their range two rows would be written and read at once.  The
+    workspace is missing in every call, so that what is not refused ends there."""
+    base, M, V = 1 << 20, 4, 32
+    dtype = 0 if es == 2 else 1
+
+    def want(off, ld, ldd):
+        if off == 0 and ld == ldd:
+            return -5
+        rows = {i * ld + v for i in range(M) for v in range(V)}
+        grads = {off + i * ldd + v for i in range(M) for v in range(V)}
+        if ld == ldd:
+            return -2 if rows & grads else -5
+        lo, hi = (0, (M - 1) * ld + V), (off, off + (M - 1) * ldd + V)
+        return -2 if lo[0] < hi[1] and hi[0] < lo[1] else -5
+
+    for ld, ldd in [(32, 32), (40, 40), (64, 64), (80, 80), (64, 32), (32, 64)]:
+        for off in range(-330, 331):
+            g, l = P(base + off * es), P(base)
+            assert lib.policy_loss(l, dtype, M, V, ld, 1.0, FAKE, FAKE, FAKE, None, None, 0.2, 0.2, 0.0, 1.0, FAKE,
+                                   FAKE, g, ldd, None, 0, None) == want(off, ld, ldd), (ld, ldd, off)
+            assert lib.preference_loss(l, dtype, M, V, ld, 1.0, FAKE, FAKE, 1, None, 0, 0.1, 0.0, 0.0, 0, 1.0, FAKE,
+                                       FAKE, FAKE, g, ldd, None, 0, None) == want(off, ld, ldd), (ld, ldd, off)
+    # one row has no pitch
+    assert lib.policy_loss(P(base), dtype, 1, V, 32, 1.0, FAKE, FAKE, FAKE, None, None, 0.2, 0.2, 0.0, 1.0, FAKE, FAKE,
+                           P(base), 64, None, 0, None) == -5
+
+
 def test_loss_workspace(lib):
     assert ops.loss_workspace_bytes(1) >= 16 and ops.loss_workspace_bytes(1000) >= 16000
     assert ops.loss_workspace_bytes(0) == 0 and ops.loss_workspace_bytes((1 << 24) + 1) == 0
