@@ -1091,6 +1091,7 @@ __global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const Policy
     T* o0 = static_cast<T*>(a.out);
     const int zlog = __ffs((int)z) - 1, M = (int)a.M, V = a.V, G = gridDim.x >> zlog;     // z is a power of two
 
+    const bool ragged = (a.ld * (int64_t)sizeof(T)) % 16 != 0;
     int waited = 0;
     uint32_t nth = 0;                                     // rows of this cluster so far
     // this CTA's vectors of a row, and their copy into buf (one thread)
@@ -1167,11 +1168,17 @@ __global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const Policy
         MS ms{0.f, 1.f};
         if (live) {
             if (e1 >= 0) x1 = El<T>::get(x[e1]);
-            // buf behind the copy is -inf: a row's part differs from another one's by fewer than 16 vectors
-            // (its alignment moves one, and dealing them out to the CTAs up to z - 1 more), and each is
-            // read by the one thread that clears it here
-            const int past = nv > 0 ? nv + ((tid - nv) & (NT - 1)) : tid;
-            if (past - nv < 16 && past < NV * NT) buf[past] = none;
+            // buf behind the copy is -inf.  Where the pitch is a multiple of 16 bytes all rows have the same
+            // vectors; else a row's part differs from another one's by fewer than 16 of them (its alignment
+            // moves one, and dealing them out to the CTAs up to z - 1 more), and each is read by the one
+            // thread that clears it here
+            if (ragged) {
+                const int past = nv > 0 ? nv + ((tid - nv) & (NT - 1)) : tid;
+                if (past - nv < 16 && past < NV * NT) {
+                    buf[past] = none;
+                    tc::fence_proxy_async();              // a later copy that reaches this far comes after it
+                }
+            }
             tc::mbar_wait(bar, waited & 1, abort);
             ++waited;
 #pragma unroll
