@@ -120,7 +120,7 @@ __device__ __forceinline__ void add1(MS& a, float x, float c) {
 }
 
 constexpr int kRowThreads = 512;                 // largest block of the row kernels
-constexpr int kMaxZ = 8;                         // CTAs of a cluster that share a row
+constexpr int kMaxZ = 16;                        // CTAs of a cluster that share a row, at most
 
 __device__ __forceinline__ uint32_t cluster_size() {
     uint32_t z;
@@ -175,7 +175,7 @@ __device__ __forceinline__ MS row_total(MS v, float c, RowShared& sh, uint32_t r
 }
 
 // ---------------------------------------------------------------------------
-// rows held in registers, the next one on its way into shared memory
+// rows held in registers
 // ---------------------------------------------------------------------------
 // Sum of 2^(c l) over a set of logits as s 2^k with an integer k, so that
 // t = c l - k is one rounding: c l - k in one fused multiply-add, to which the
@@ -187,10 +187,6 @@ struct __align__(8) KS {
 };
 
 constexpr float kTop = 0x1p100f;
-constexpr uint32_t kBulk = 16384;                // bytes per bulk copy
-// CTAs per SM of the kernels that hold a row in registers: as many as leave a
-// thread its NV vectors and 60 registers more (without spills)
-constexpr int engine_ctas(int nt, int nv) { return 65536 / (nt * (nv <= 4 ? 72 : nv <= 8 ? 80 : nv <= 16 ? 128 : 255)); }
 
 __device__ __forceinline__ float round_k(float m, float c) { return rintf(fminf(fmaxf(m * c, -kTop), kTop)); }
 
@@ -267,82 +263,55 @@ __device__ __forceinline__ KS warp_total(KS v) {
     return o;
 }
 
-struct EngineShared {
+struct BlockShared {
     KS warp[kRowThreads / 32];
-    KS rank[2][kMaxZ];                           // written by the CTAs of the cluster, by row parity
+    KS rank[kMaxZ];                              // written by the CTAs of the cluster
     RowShared careful;
     float4 row;                                  // what warp 0 made of the row
-    int tick[2];                                 // the row after the next two, by row parity
-    float edge[16];                              // the row's head and tail elements
-    int issued;                                  // copies started
-    unsigned long long bar;                      // the row's copy
-    unsigned long long xbar[2];                  // what the cluster's CTAs send, by row parity
+    unsigned long long xbar;                     // what the cluster's CTAs send
     int abort;
 };
 
-// What the CTAs of a cluster tell one another about a row: every CTA sends its
-// (k, s) to all of them, and rank 0 the ticket, by asynchronous stores that
-// complete on the receiver's barrier of the row's parity.  One warp sends and
-// waits; the block learns of it at its next barrier.  (A cluster barrier of all
-// threads in its place took ~1 us more per row.)  Two parities are enough: a CTA
-// sends for a row only after it has received all of the row before.
-__device__ __forceinline__ void engine_init(EngineShared& sh) {
+// The CTAs of a cluster that share a row tell one another their sums: every
+// CTA sends its (k, s) to all of them by asynchronous stores that complete on
+// the receiver's barrier.  One warp sends and waits; the block learns of it at
+// its next barrier.  (A cluster barrier of all threads in its place took ~1 us
+// more per row.)
+__device__ __forceinline__ void exchange_init(BlockShared& sh) {
     if (threadIdx.x == 0) {
         sh.abort = 0;
-        sh.issued = 0;
-        tc::mbar_init(smem_u32(&sh.bar), 1);
-        tc::mbar_init(smem_u32(&sh.xbar[0]), 1);
-        tc::mbar_init(smem_u32(&sh.xbar[1]), 1);
+        tc::mbar_init(smem_u32(&sh.xbar), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
 }
 
-// Warp 0 of every CTA: (k, s) of all ranks added up; the ticket is in
-// sh.tick[row & 1] behind the block's next barrier.  `row` counts the rows of
-// this cluster from 0.
-__device__ __forceinline__ KS engine_exchange(KS v, EngineShared& sh, uint32_t rank, uint32_t z, uint32_t row,
-                                              int tick) {
-    const int lane = threadIdx.x & 31, parity = row & 1;
-    if (z == 1) {
-        if (lane == 0) sh.tick[parity] = tick;   // lane 0 drew it
-        return v;
-    }
-    tick = __shfl_sync(0xffffffffu, tick, 0);
-    const uint32_t xb = smem_u32(&sh.xbar[parity]);
-    if (lane == 0) tc::mbar_expect_tx(xb, z * 8 + 4);
+// Warp 0 of every CTA: (k, s) of all ranks added up.
+__device__ __forceinline__ KS exchange(KS v, BlockShared& sh, uint32_t rank, uint32_t z) {
+    if (z == 1) return v;
+    const int lane = threadIdx.x & 31;
+    const uint32_t xb = smem_u32(&sh.xbar);
+    if (lane == 0) tc::mbar_expect_tx(xb, z * 8);
     if (lane < (int)z) {
-        const uint32_t bar = mapa(xb, lane);
         const unsigned long long ks = (unsigned long long)__float_as_uint(v.s) << 32 | __float_as_uint(v.k);
         asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
-                         mapa(smem_u32(&sh.rank[parity][rank]), lane)),
-                     "l"(ks), "r"(bar)
+                         mapa(smem_u32(&sh.rank[rank]), lane)),
+                     "l"(ks), "r"(mapa(xb, lane))
                      : "memory");
-        if (rank == 0)
-            asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
-                             mapa(smem_u32(&sh.tick[parity]), lane)),
-                         "r"(tick), "r"(bar)
-                         : "memory");
     }
     __syncwarp();
-    tc::mbar_wait(xb, (row >> 1) & 1, &sh.abort);
-    return warp_total(lane < (int)z ? sh.rank[parity][lane] : KS{-kTop, 0.f});
+    tc::mbar_wait(xb, 0, &sh.abort);
+    return warp_total(lane < (int)z ? sh.rank[lane] : KS{-kTop, 0.f});
 }
 
 // The row's (k, s) in warp 0 of every CTA of the cluster (the other warps
 // return what they have at once).
-__device__ __forceinline__ KS engine_total(KS v, EngineShared& sh, uint32_t rank, uint32_t z, uint32_t row, int tick) {
+__device__ __forceinline__ KS block_total(KS v, BlockShared& sh, uint32_t rank, uint32_t z) {
     const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     v = warp_total(v);
     if (lane == 0) sh.warp[threadIdx.x >> 5] = v;
     __syncthreads();
-    if (threadIdx.x < 32) v = engine_exchange(warp_total(lane < nw ? sh.warp[lane] : KS{-kTop, 0.f}), sh, rank, z, row, tick);
+    if (threadIdx.x < 32) v = exchange(warp_total(lane < nw ? sh.warp[lane] : KS{-kTop, 0.f}), sh, rank, z);
     return v;
-}
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
-                 : "memory");
 }
 
 // One CTA's part of a row: the sum of its exponentials, and its gradient.
@@ -400,7 +369,7 @@ __device__ __forceinline__ void grad_pass(uint4 (&v)[NV], float x1, float ly, T*
 // The careful form of one row, read again from memory (rows out of k's range:
 // rare): this CTA's vectors [v0, v1) and, in rank 0, the head and the tail.
 template <typename T>
-__device__ __noinline__ MS careful_total(const T* x, int V, int v0, int v1, float c, EngineShared& sh,
+__device__ __noinline__ MS careful_total(const T* x, int V, int v0, int v1, float c, BlockShared& sh,
                                          uint32_t rank, uint32_t z) {
     const Row<T> sp(x, V);
     MS ms{-INFINITY, 0.f};
@@ -468,13 +437,14 @@ __device__ __noinline__ void scalar_grad(const T* x, T* o, int V, int y, int v0,
 // ---------------------------------------------------------------------------
 // For few vectors a thread, the barriers of a large block and a row's latency
 // took most of the time.  Rows of up to 32 x 16 vectors take a warp, without
-// any barrier, rows of up to 128 x 16 a block of 128 threads; as many of them
-// are in flight as the registers hold, and the hardware deals them out.
-constexpr int kShortThreads = 128;
+// any barrier (65536 x 500 bf16: log-probabilities 90 us with 256 threads a row,
+// 25 with a warp), rows of up to 128 x 16 a block of 128 threads; as many of
+// them are in flight as the registers hold, and the hardware deals them out.
+constexpr int kBlockThreads = 128;
 
 struct ShortShared {
-    KS warp[kShortThreads / 32];
-    MS careful[kShortThreads / 32];
+    KS warp[kBlockThreads / 32];
+    MS careful[kBlockThreads / 32];
 };
 
 template <typename T, int NT, int NV>
@@ -576,11 +546,11 @@ __device__ __forceinline__ void put_logp(const RowArgs& a, int64_t row, double l
 }
 
 template <typename T, int NT, int NV>
-__global__ void __launch_bounds__(kShortThreads) k_token_logprob_short(const RowArgs a) {
+__global__ void __launch_bounds__(kBlockThreads) k_token_logprob_short(const RowArgs a) {
     __shared__ ShortShared sh;
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t row = (int64_t)blockIdx.x * (kShortThreads / NT) + threadIdx.x / NT;
+    const int64_t row = (int64_t)blockIdx.x * (kBlockThreads / NT) + threadIdx.x / NT;
     if (row >= a.M) return;
     const bool first = (threadIdx.x & (NT - 1)) == 0;
     const int64_t y = a.targets[row];
@@ -606,9 +576,9 @@ constexpr float kSlack = 32.f;                   // how far a term's exponent ma
 // k moves only when a logit comes that is more than 2^kSlack above it.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) k_token_logprob(const RowArgs a) {
-    __shared__ EngineShared sh;
+    __shared__ BlockShared sh;
     const uint32_t rank = cluster_rank(), z = cluster_size();
-    engine_init(sh);
+    exchange_init(sh);
     if (z > 1) cluster_arrive();
     grid_dep_wait();
     grid_dep_launch();
@@ -673,7 +643,7 @@ __global__ void __launch_bounds__(kRowThreads) k_token_logprob(const RowArgs a) 
     un2(s2, sa, sb);
     acc.s = sa + sb;
     if (z > 1) cluster_wait();                   // every CTA of the cluster runs
-    const KS t = engine_total(acc, sh, rank, z, 0, 0);
+    const KS t = block_total(acc, sh, rank, z);
     if (tid == 0) sh.row.x = in_range(t.s) ? 1.f : 0.f;
     __syncthreads();
     if (sh.row.x != 0.f) {
@@ -1042,7 +1012,6 @@ struct PolicyArgs {
     float4* part;                // [M] weighted (loss, policy, kl, clipped)
     void* out;                   // gradient, or null; may be the logits themselves (ldo == ld)
     int64_t ldo;
-    int* ticket;                 // 0 before the launch; null: the rows are dealt out in turn
 };
 
 // The row's loss terms (written by the thread that is told to) and d loss /
@@ -1062,194 +1031,99 @@ __device__ __forceinline__ float policy_row(const PolicyArgs& a, int row, float 
 }
 
 // A row's gradient depends on that row alone, so each row is read once, held
-// in registers (NV vectors per thread of a cluster of z CTAs), and its
-// gradient written: the 2 M V elements that cannot be done without.  The
-// grid is what the SMs hold, and a cluster has the bulk copy of its next row
-// in flight while it works on one, so that the loads do not wait for the two
-// passes and the reduction.  With many rows the clusters draw them from a
-// counter, three ahead of the work: dealt out in turn, the second CTA of an
-// SM, whose warps are issued after the first one's, ended a quarter later.
-template <typename T, int NT, int NV>
-__global__ void __launch_bounds__(NT, engine_ctas(NT, NV)) k_policy(const PolicyArgs a) {
-    extern __shared__ __align__(128) uint4 buf[];         // this CTA's part of the next row
-    __shared__ EngineShared sh;
-    constexpr int N = El<T>::N;
+// in registers (NV vectors per thread of a cluster of z blocks), and its
+// gradient written: the 2 M V elements that cannot be done without.  Three to
+// five blocks of an SM are each at another point of load, two passes and
+// store, which hides the barriers and the latency of each; a persistent block
+// of 256 threads with the bulk copy of its next row in flight moved less (7456
+// x 72000 bf16: 652 us, this one 399; 16777 x 32000: 398 and 369).  1 GB of
+// logits: bf16 5.8 TB/s of reads and writes at 32000 (its exponentials, two an
+// element, share the time with the memory), fp32 6.6 TB/s, the rate of a copy.
+template <typename T, int NV>
+__global__ void __launch_bounds__(kBlockThreads) k_policy_block(const PolicyArgs a) {
+    constexpr int NT = kBlockThreads;
+    __shared__ BlockShared sh;
     const uint32_t rank = cluster_rank(), z = cluster_size();
-    const int tid = threadIdx.x;
-    const uint32_t bar = smem_u32(&sh.bar);
-    volatile int* abort = &sh.abort;
-    const uint4 none = make_uint4(Pairs<T>::kNegInf, Pairs<T>::kNegInf, Pairs<T>::kNegInf, Pairs<T>::kNegInf);
-#pragma unroll
-    for (int u = 0; u < NV; ++u) buf[tid + u * NT] = none;
-    engine_init(sh);
-    tc::fence_proxy_async();                              // the copies into buf come after these stores
-    __syncthreads();
-    if (z > 1) cluster_arrive();
+    const int tid = threadIdx.x, V = a.V;
+    if (z > 1) {
+        exchange_init(sh);
+        cluster_arrive();
+    }
     grid_dep_wait();
     grid_dep_launch();
-    const T* x0 = static_cast<const T*>(a.logits);
-    T* o0 = static_cast<T*>(a.out);
-    const int zlog = __ffs((int)z) - 1, M = (int)a.M, V = a.V, G = gridDim.x >> zlog;     // z is a power of two
-
-    const bool ragged = (a.ld * (int64_t)sizeof(T)) % 16 != 0;
-    int waited = 0;
-    uint32_t nth = 0;                                     // rows of this cluster so far
-    // this CTA's vectors of a row, and their copy into buf (one thread)
-    auto span = [&](const Row<T>& sp, int& v0, int& v1) {
-        const int per = (sp.nv + (int)z - 1) >> zlog;
-        v0 = (int)rank * per;
-        v1 = v0 + per < sp.nv ? v0 + per : sp.nv;
-    };
-    auto load = [&](int row) {
-        const T* x = x0 + row * a.ld;
-        const Row<T> sp(x, V);
-        int v0, v1;
-        span(sp, v0, v1);
-        const uint32_t bytes = v1 > v0 ? (uint32_t)(v1 - v0) * 16u : 0u;
-        if (*abort) return;                               // nothing is waited for any more
-        ++sh.issued;
-        tc::mbar_expect_tx(bar, bytes);
-        for (uint32_t b = 0; b < bytes; b += kBulk)
-            bulk_load(smem_u32(buf) + b, reinterpret_cast<const uint8_t*>(x + sp.head + v0 * N) + b,
-                      bytes - b < kBulk ? bytes - b : kBulk, bar);
-    };
-    // the row's target, -1 where it takes no part: loaded two rows ahead, looked at one row ahead
-    int64_t raw_y = -1;
-    float raw_w = 0.f;
-    auto fetch = [&](int row) {
-        raw_y = row < M ? a.targets[row] : -1;
-        raw_w = row < M ? a.weight[row] : 0.f;
-    };
-    auto target = [&] { return raw_y >= 0 && raw_y < V && raw_w != 0.f ? (int)raw_y : -1; };
-
-    // what a row's loss takes, one value a lane: the logit of the target, the advantage, the weight, and the
-    // two log-probabilities; loaded a row ahead like the row itself
-    auto meta = [&](int row, int y) {
-        float m = 0.f;
-        const int lane = tid & 31;
-        if (y >= 0) {
-            if (lane == 0) m = El<T>::get(x0[row * a.ld + y]);
-            const float* p = lane == 1 ? a.adv : lane == 2 ? a.weight : lane == 3 ? a.old_logp
-                           : lane == 4 ? a.ref_logp : nullptr;
-            if (p) m = p[row];
-        }
-        return m;
-    };
-
-    int row = blockIdx.x >> zlog;
-    fetch(row);
-    int y = target();
-    int nrow = row + G, row2 = row + 2 * G, tick;
-    fetch(nrow);
-    float mt = meta(row, y);
-    if (y >= 0 && tid == 0) load(row);
-    if (z > 1) cluster_wait();                            // every CTA of the cluster runs
-    for (; row < M; row = nrow, nrow = row2, row2 = tick) {
-        const int ny = target();
-        fetch(row2);
-        tick = row2 + G;
-        if (a.ticket != nullptr && rank == 0 && tid == 0) tick = 3 * G + atomicAdd(a.ticket, 1);
-        const float nmt = meta(nrow, ny);
-        const bool live = y >= 0, nlive = ny >= 0;
-        const T* x = x0 + row * a.ld;
-        T* o = o0 + row * a.ldo;
-        const Row<T> sp(x, V);
-        const bool same = a.out == nullptr ||
-                          ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
-        int v0, v1;
-        span(sp, v0, v1);
-        const int nv = v1 - v0;                           // none where negative
-        // the one element of the head or the tail that this thread holds
-        const int e1 = rank != 0 ? -1 : tid < sp.head ? tid
-                     : tid >= 8 && tid < 8 + sp.tail ? V - sp.tail + tid - 8 : -1;
-        uint4 v[NV];
-        float x1 = -INFINITY, ly = 0.f, g = 0.f, k = 0.f, q = 0.f;
-        bool careful = false;
-        MS ms{0.f, 1.f};
-        if (live) {
-            if (e1 >= 0) x1 = El<T>::get(x[e1]);
-            // buf behind the copy is -inf.  Where the pitch is a multiple of 16 bytes all rows have the same
-            // vectors; else a row's part differs from another one's by fewer than 16 of them (its alignment
-            // moves one, and dealing them out to the CTAs up to z - 1 more), and each is read by the one
-            // thread that clears it here
-            if (ragged) {
-                const int past = nv > 0 ? nv + ((tid - nv) & (NT - 1)) : tid;
-                if (past - nv < 16 && past < NV * NT) {
-                    buf[past] = none;
-                    tc::fence_proxy_async();              // a later copy that reaches this far comes after it
-                }
-            }
-            tc::mbar_wait(bar, waited & 1, abort);
-            ++waited;
+    const int row = blockIdx.x / z;
+    const T* x = static_cast<const T*>(a.logits) + row * a.ld;
+    T* o = static_cast<T*>(a.out) + row * a.ldo;
+    const Row<T> sp(x, V);
+    const int per = (sp.nv + (int)z - 1) / (int)z, v0 = (int)rank * per, v1 = v0 + per < sp.nv ? v0 + per : sp.nv;
+    const int nv = v1 - v0;                               // none where negative
+    const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head) + v0;
+    uint4 v[NV];
 #pragma unroll
-            for (int u = 0; u < NV; ++u) v[u] = buf[tid + u * NT];
-            if (nlive) {                                  // once all have read buf, the next row may come
-                if (tid < 32) {
-                    asm volatile("barrier.cta.sync 1, %0;" ::"n"(NT) : "memory");
-                    if (tid == 0) load(nrow);
-                } else {
-                    asm volatile("barrier.cta.arrive 1, %0;" ::"n"(NT) : "memory");
-                }
-            }
-            const KS acc = sum_pass<T, NV>(v, x1, a.c, a.c_lo);
-            const KS t = engine_total(acc, sh, rank, z, nth, tick);
-            auto row_loss = [&](float lp) {
-                return policy_row(a, row, lp, __shfl_sync(0xffffffffu, mt, 1), __shfl_sync(0xffffffffu, mt, 2),
-                                  __shfl_sync(0xffffffffu, mt, 3), __shfl_sync(0xffffffffu, mt, 4),
-                                  rank == 0 && tid == 0);
-            };
-            ly = __shfl_sync(0xffffffffu, mt, 0);
-            if (tid < 32) {
-                // the loss of the row and its derivative, by one warp: sixteen took most of the issue slots
-                const float lp = (fmaf(ly, a.c_lo, fmaf(ly, a.c, -t.k)) - log2f(t.s)) * kLn2;
-                const bool fine = in_range(t.s);
-                g = fine ? row_loss(lp > 0.f ? 0.f : lp) : 0.f;
-                if (tid == 0) sh.row = make_float4(t.k, -g / t.s, g, fine ? 0.f : 1.f);
-            }
-            __syncthreads();
-            tick = sh.tick[nth & 1];
-            const float4 rv = sh.row;
-            k = rv.x; q = rv.y; g = rv.z;
-            careful = rv.w != 0.f;
-            if (careful) {
-                // out of k's range, NaN, or nothing above -inf
-                ms = careful_total(x, V, v0, v1, a.c, sh, rank, z);
-                g = row_loss((float)logp_of(ly, ms, a.tau));
-            }
-        } else {
-            if (nlive && tid == 0) load(nrow);
-            __syncthreads();                              // the ticket of the row before has been read
-            if (tid < 32) engine_exchange(KS{0.f, 0.f}, sh, rank, z, nth, tick);
-            __syncthreads();
-            tick = sh.tick[nth & 1];
-            if (rank == 0 && tid == 0) {
-                a.logp[row] = 0.f;
-                a.part[row] = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+    for (int u = 0; u < NV; ++u)
+        v[u] = tid + NT * u < nv ? ld_v4(xv + tid + NT * u)
+                                 : make_uint4(Pairs<T>::kNegInf, Pairs<T>::kNegInf, Pairs<T>::kNegInf,
+                                              Pairs<T>::kNegInf);
+    const int64_t y64 = a.targets[row];
+    const float w = a.weight[row];
+    const int y = y64 >= 0 && y64 < V && w != 0.f ? (int)y64 : -1;
+    if (y < 0) {
+        if (rank == 0 && tid == 0) {
+            a.logp[row] = 0.f;
+            a.part[row] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (a.out == nullptr) {
-        } else if (g == 0.f) {                            // padding, or a loss that is flat here
-            zero_row(o, V, v0, v1, rank);
-        } else if (careful || !same) {
-            scalar_grad(x, o, V, y, v0, v1, a.c, careful, ms, k, q, g, rank);
-        } else {
-            grad_pass<T, NT, NV>(v, x1, ly, o, sp, v0, nv, e1, y, a.c, k, q, g);
-        }
-        ++nth;
-        y = ny;
-        mt = nmt;
+        if (a.out != nullptr) zero_row(o, V, v0, v1, rank);
+        if (z > 1) cluster_wait();
+        return;
     }
-    // after an expired wait: the copy in flight lands before the CTA leaves
-    if (tid == 0 && *abort && sh.issued > 0) tc::mbar_drain(bar, (sh.issued - 1) & 1);
+    const float A = a.adv[row], old = a.old_logp ? a.old_logp[row] : 0.f, ref = a.ref_logp ? a.ref_logp[row] : 0.f;
+    const float ly0 = El<T>::get(x[y]);
+    // the one element of the head or the tail that this thread holds
+    const int e1 = rank != 0 ? -1 : tid < sp.head ? tid
+                 : tid >= 8 && tid < 8 + sp.tail ? V - sp.tail + tid - 8 : -1;
+    const float x1 = e1 >= 0 ? El<T>::get(x[e1]) : -INFINITY;
+    KS t = sum_pass<T, NV>(v, x1, a.c, a.c_lo);
+    // in place, another CTA of the cluster writes the target's gradient once it has this one's sum: the
+    // logit has arrived when it is handed on here, before that
+    const float ly = __shfl_sync(0xffffffffu, ly0, 0);
+    if (z > 1) cluster_wait();                            // every CTA of the cluster runs
+    t = block_total(t, sh, rank, z);
+    if (tid < 32) {
+        // the loss of the row and its derivative, by one warp
+        const float lp = (fmaf(ly, a.c_lo, fmaf(ly, a.c, -t.k)) - log2f(t.s)) * kLn2;
+        const bool fine = in_range(t.s);
+        const float g = fine ? policy_row(a, row, lp > 0.f ? 0.f : lp, A, w, old, ref, rank == 0 && tid == 0) : 0.f;
+        if (tid == 0) sh.row = make_float4(t.k, -g / t.s, g, fine ? 0.f : 1.f);
+    }
+    __syncthreads();
+    const float4 rv = sh.row;
+    const float k = rv.x, q = rv.y;
+    float g = rv.z;
+    const bool careful = rv.w != 0.f;
+    MS ms{0.f, 1.f};
+    if (careful) {
+        // out of k's range, NaN, or nothing above -inf
+        ms = careful_total(x, V, v0, v1, a.c, sh, rank, z);
+        g = policy_row(a, row, (float)logp_of(ly, ms, a.tau), A, w, old, ref, rank == 0 && tid == 0);
+    }
+    if (a.out == nullptr) return;
+    const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
+    if (g == 0.f) {                                       // a loss that is flat here
+        zero_row(o, V, v0, v1, rank);
+    } else if (careful || !same) {
+        scalar_grad(x, o, V, y, v0, v1, a.c, careful, ms, k, q, g, rank);
+    } else {
+        grad_pass<T, NT, NV>(v, x1, ly, o, sp, v0, nv, e1, y, a.c, k, q, g);
+    }
 }
 
-// The same for short rows.
+// The same for short rows, a warp each.
 template <typename T, int NT, int NV>
-__global__ void __launch_bounds__(kShortThreads) k_policy_short(const PolicyArgs a) {
+__global__ void __launch_bounds__(kBlockThreads) k_policy_short(const PolicyArgs a) {
     __shared__ ShortShared sh;
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t row = (int64_t)blockIdx.x * (kShortThreads / NT) + threadIdx.x / NT;
+    const int64_t row = (int64_t)blockIdx.x * (kBlockThreads / NT) + threadIdx.x / NT;
     if (row >= a.M) return;
     const int id = threadIdx.x & (NT - 1), V = a.V;
     const T* x = static_cast<const T*>(a.logits) + row * a.ld;

@@ -1093,12 +1093,10 @@ void split_c(float tau, float* c, float* c_lo) {
 }
 
 template <typename KArg>
-int launch_rows(void (*kern)(KArg), int64_t rows, int z, int threads, cudaStream_t st, const KArg& args,
-                int smem = 0) {
+int launch_rows(void (*kern)(KArg), int64_t rows, int z, int threads, cudaStream_t st, const KArg& args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(rows * z));
     cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1118,15 +1116,24 @@ int launch_rows(void (*kern)(KArg), int64_t rows, int z, int threads, cudaStream
 // lane (65536 x 2000 bf16: 125 us with 128 threads, 47 with a warp).
 int row_threads(int64_t nv) { return nv <= 4096 ? 128 : 256; }
 
-// Longest rows in vectors that a warp, a block of 128 threads takes in registers.
+// Longest rows in vectors that a warp, a block of 128 threads takes in registers
+// to add up a row (longer ones go through them four vectors at a time: 16777 x
+// 32000 bf16 164 us, held in registers 180).
 constexpr int kWarpRow = 32 * 16, kBlockRow = 128 * 16;
 
-int64_t short_ctas(int64_t M, int nv) { return nv <= kWarpRow ? cdiv(M, (int64_t)loss::kShortThreads / 32) : M; }
+int64_t warp_ctas(int64_t M) { return cdiv(M, (int64_t)loss::kBlockThreads / 32); }
 
-// The kernel for a short row of nv vectors: 2, 4, 8, 16 vectors a lane, then 8, 16 a thread.
-#define QLORA_SHORT_KERNEL(KERN, T, nv)                                                                  \
-    ((nv) <= 64 ? KERN<T, 32, 2> : (nv) <= 128 ? KERN<T, 32, 4> : (nv) <= 256 ? KERN<T, 32, 8>           \
-     : (nv) <= 512 ? KERN<T, 32, 16> : (nv) <= 1024 ? KERN<T, 128, 8> : KERN<T, 128, 16>)
+// The kernel for a row of nv vectors by the vectors per lane of a warp, per
+// thread of a block.  Empty ones cost the arithmetic of full ones (52428 x
+// 10240 bf16 with 10 and with 16 per thread: log-probabilities 151 and 219 us),
+// so the steps are a quarter to a half.
+#define QLORA_WARP_KERNEL(KERN, T, nv)                                                                      \
+    ((nv) <= 64 ? KERN<T, 32, 2> : (nv) <= 96 ? KERN<T, 32, 3> : (nv) <= 128 ? KERN<T, 32, 4>               \
+     : (nv) <= 192 ? KERN<T, 32, 6> : (nv) <= 256 ? KERN<T, 32, 8> : (nv) <= 384 ? KERN<T, 32, 12>          \
+     : KERN<T, 32, 16>)
+#define QLORA_BLOCK_KERNEL(KERN, T, nv)                                                                     \
+    ((nv) <= 640 ? KERN<T, 128, 5> : (nv) <= 768 ? KERN<T, 128, 6> : (nv) <= 1024 ? KERN<T, 128, 8>         \
+     : (nv) <= 1280 ? KERN<T, 128, 10> : (nv) <= 1536 ? KERN<T, 128, 12> : KERN<T, 128, 16>)
 
 int launch_logprob(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float tau, const int64_t* targets,
                    float* logp, float2* stats, double* lpd, int sms, cudaStream_t st) {
@@ -1136,59 +1143,57 @@ int launch_logprob(const void* logits, int dtype, int64_t M, int64_t V, int64_t 
     a.targets = targets; a.logp = logp; a.stats = stats; a.lpd = lpd;
     const int64_t nv = V * (int64_t)logit_bytes(dtype) / 16;
     int z = 1;
-    // with few rows a row is better split over a cluster than left to one small block
-    if (nv <= kWarpRow || (nv <= kBlockRow && 2 * M > 4 * (int64_t)sms)) {
-        const int64_t ctas = short_ctas(M, (int)nv);
+    if (nv <= kWarpRow)
         return dtype == QLORA_LOGITS_FP32
-                   ? launch_rows<loss::RowArgs>(QLORA_SHORT_KERNEL(loss::k_token_logprob_short, float, nv), ctas, 1,
-                                                loss::kShortThreads, st, a)
-                   : launch_rows<loss::RowArgs>(QLORA_SHORT_KERNEL(loss::k_token_logprob_short, uint16_t, nv), ctas, 1,
-                                                loss::kShortThreads, st, a);
-    }
+                   ? launch_rows<loss::RowArgs>(QLORA_WARP_KERNEL(loss::k_token_logprob_short, float, nv), warp_ctas(M),
+                                                1, loss::kBlockThreads, st, a)
+                   : launch_rows<loss::RowArgs>(QLORA_WARP_KERNEL(loss::k_token_logprob_short, uint16_t, nv),
+                                                warp_ctas(M), 1, loss::kBlockThreads, st, a);
+    // with few rows a row is better split over a cluster than left to one small block
+    if (nv <= kBlockRow && 2 * M > 4 * (int64_t)sms)
+        return dtype == QLORA_LOGITS_FP32
+                   ? launch_rows<loss::RowArgs>(QLORA_BLOCK_KERNEL(loss::k_token_logprob_short, float, nv), M, 1,
+                                                loss::kBlockThreads, st, a)
+                   : launch_rows<loss::RowArgs>(QLORA_BLOCK_KERNEL(loss::k_token_logprob_short, uint16_t, nv), M, 1,
+                                                loss::kBlockThreads, st, a);
     const int threads = row_threads(nv);
     // a row is split over a cluster while the rows alone would not fill the SMs
-    while (z < loss::kMaxZ && M * z * 2 <= 4 * (int64_t)sms && nv >= 2 * z * threads) z *= 2;
+    while (z < 8 && M * z * 2 <= 4 * (int64_t)sms && nv >= 2 * z * threads) z *= 2;
     return dtype == QLORA_LOGITS_FP32 ? launch_rows<loss::RowArgs>(loss::k_token_logprob<float>, M, z, threads, st, a)
                                       : launch_rows<loss::RowArgs>(loss::k_token_logprob<uint16_t>, M, z, threads, st, a);
 }
 
-template <typename T, int NT, int NV>
-int launch_policy_nv(loss::PolicyArgs a, int z, int sms, cudaStream_t st) {
-    static std::atomic<int> set[64];
-    constexpr int smem = NV * NT * 16;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QLORA_ERR_DEVICE;
-    if (set[dev].load() == 0) {
-        if (cudaFuncSetAttribute(loss::k_policy<T, NT, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-            cudaSuccess)
-            return QLORA_ERR_LAUNCH;
-        set[dev].store(1);
-    }
-    const int64_t slots = (int64_t)sms * loss::engine_ctas(NT, NV) / z;
-    // the counter is cleared by an operation of its own, so only where each cluster takes several rows
-    if (a.M <= 4 * slots) a.ticket = nullptr;
-    else if (cudaMemsetAsync(a.ticket, 0, sizeof(int), st) != cudaSuccess) return QLORA_ERR_LAUNCH;
-    return launch_rows<loss::PolicyArgs>(loss::k_policy<T, NT, NV>, a.M < slots ? a.M : slots, z, NT, st, a, smem);
+template <typename T, int NV>
+int launch_policy_block(const loss::PolicyArgs& a, int z, cudaStream_t st) {
+    if (z > 8 && cudaFuncSetAttribute(loss::k_policy_block<T, NV>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                     cudaSuccess)
+        return QLORA_ERR_LAUNCH;
+    return launch_rows<loss::PolicyArgs>(loss::k_policy_block<T, NV>, a.M, z, loss::kBlockThreads, st, a);
 }
 
-// Threads and vectors per thread: a row is split over a cluster of z CTAs
-// where it does not fit 16 vectors a thread, or while the rows alone would not
-// give every SM two CTAs.
+// Vectors per thread: a row is split over a cluster of z CTAs where it does
+// not fit 32 vectors a thread (16 vectors and twice the CTAs: 22369 x 24000 bf16
+// 363 us against 339, 8194 x 32760 fp32 334 against 331), or while the rows
+// alone would not give every SM four CTAs (296 x 32000 bf16: 12.5 us split, 14.5
+// not).  The steps of the count are fine for the reason above (10682 x 50256
+// bf16: 411 us with 26, 421 with 28).
 template <typename T>
 int launch_policy(const loss::PolicyArgs& a, int sms, cudaStream_t st) {
     const int nv = a.V * (int)sizeof(T) / 16;
-    if (nv <= kWarpRow || (nv <= kBlockRow && 2 * a.M > 4 * (int64_t)sms))
-        return launch_rows<loss::PolicyArgs>(QLORA_SHORT_KERNEL(loss::k_policy_short, T, nv), short_ctas(a.M, nv), 1,
-                                             loss::kShortThreads, st, a);
+    if (nv <= kWarpRow)
+        return launch_rows<loss::PolicyArgs>(QLORA_WARP_KERNEL(loss::k_policy_short, T, nv), warp_ctas(a.M), 1,
+                                             loss::kBlockThreads, st, a);
+    constexpr int bt = loss::kBlockThreads;
     int z = 1;
-    while (z < loss::kMaxZ && (nv > z * 256 * 16 || (a.M * z * 2 <= 2 * (int64_t)sms && nv >= 2 * z * 256))) z *= 2;
-    const int per = (nv + z - 1) / z;
-    if (per <= 256) return launch_policy_nv<T, 256, 1>(a, z, sms, st);
-    if (per <= 512) return launch_policy_nv<T, 256, 2>(a, z, sms, st);
-    if (per <= 1024) return launch_policy_nv<T, 256, 4>(a, z, sms, st);
-    if (per <= 2048) return launch_policy_nv<T, 256, 8>(a, z, sms, st);
-    if (per <= 4096) return launch_policy_nv<T, 256, 16>(a, z, sms, st);
-    return launch_policy_nv<T, 256, 32>(a, z, sms, st);
+    while (z < loss::kMaxZ && nv > z * bt * 32) z *= 2;
+    while (z < 8 && a.M * z * 2 <= 4 * (int64_t)sms && nv >= 2 * z * 2 * bt) z *= 2;
+    const int n = (nv + z * bt - 1) / (z * bt);
+#define QLORA_NV(NV) \
+    if (n <= NV) return launch_policy_block<T, NV>(a, z, st);
+    QLORA_NV(2) QLORA_NV(3) QLORA_NV(4) QLORA_NV(5) QLORA_NV(6) QLORA_NV(8) QLORA_NV(10) QLORA_NV(12) QLORA_NV(14)
+    QLORA_NV(16) QLORA_NV(18) QLORA_NV(20) QLORA_NV(22) QLORA_NV(24) QLORA_NV(26) QLORA_NV(28) QLORA_NV(30)
+#undef QLORA_NV
+    return launch_policy_block<T, 32>(a, z, st);
 }
 
 }  // namespace
@@ -1659,7 +1664,7 @@ int token_logprob(const void* logits, int dtype, int64_t M, int64_t V, int64_t l
     return launch_logprob(logits, dtype, M, V, ld, logit_scale, targets, logp, nullptr, nullptr, sms, (cudaStream_t)stream);
 }
 
-size_t loss_workspace_bytes(int64_t M) { return M <= 0 || M > ((int64_t)1 << 24) ? 0 : align256((size_t)M * 24) + 256; }
+size_t loss_workspace_bytes(int64_t M) { return M <= 0 || M > ((int64_t)1 << 24) ? 0 : align256((size_t)M * 24); }
 
 int preference_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, float logit_scale,
                     const int64_t* targets, const int32_t* cu_seqlens, int64_t P, const float* ref_logp, int kind,
@@ -1747,7 +1752,6 @@ int policy_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld,
     a.targets = targets; a.old_logp = old_logp; a.ref_logp = ref_logp; a.adv = advantages; a.weight = weights;
     a.lo = 1.f - clip_low; a.hi = 1.f + clip_high; a.kl = kl_coef; a.grad_scale = grad_scale;
     a.logp = logp; a.part = static_cast<float4*>(ws); a.out = dlogits; a.ldo = ldd;
-    a.ticket = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + align256((size_t)M * 24));
     rc = dtype == QLORA_LOGITS_FP32 ? launch_policy<float>(a, sms, st) : launch_policy<uint16_t>(a, sms, st);
     if (rc != QLORA_OK) return rc;
     return launch_pdl(loss::k_policy_finish, dim3(1), dim3(loss::kFinishThreads), 0, st, (const float4*)a.part, M,

@@ -442,6 +442,17 @@ def test_policy_every_row_is_taken_once(V):
         assert (d <= 2 * HALF["bf16"] * want.dlogits[pick].float().abs() + 1e-4 * g + 1e-30).all()
 
 
+@pytest.mark.parametrize("dtype,M,V", [("bf16", 300, 8191), ("bf16", 300, 32767), ("bf16", 300, 32776), ("bf16", 3, 65551),
+                                       ("bf16", 3, 131080), ("bf16", 3, 262144), ("fp32", 300, 4095),
+                                       ("fp32", 300, 16383), ("fp32", 300, 16391), ("fp32", 3, 32779),
+                                       ("fp32", 3, 65543), ("fp32", 3, 131072), ("fp32", 40, 131079),
+                                       ("fp32", 3, 262144)])
+def test_policy_rows_of_every_width(dtype, M, V):
+    """Around the lengths from which a row is shared by one CTA more, up to a cluster of 16, at every
+    alignment of a row."""
+    _run_policy(V, M, V, dtype, ld=V + 5, off=1)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("old,ref", [(False, False), (True, False), (False, True)])
 def test_policy_without_old_or_reference(old, ref, dtype):
