@@ -698,10 +698,10 @@ struct GradArgs {
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;                     // 16-byte vectors per thread
 
-// One chunk of kGradThreads * kGradVecs vectors of row `row`: coef() is called
+// One chunk of NT * kGradVecs vectors of row `row` by NT threads: coef() is called
 // once by every thread, with the chunk's loads under way, and gives
 // d loss / d logp of the row (a row without a target is zeroed without it).
-template <typename T, typename Coef>
+template <typename T, int NT, typename Coef>
 __device__ __forceinline__ void grad_chunk(const GradArgs& a, int64_t row, int ch, Coef coef) {
     constexpr int N = El<T>::N;
     const T* x = static_cast<const T*>(a.logits) + row * a.ld;
@@ -709,8 +709,8 @@ __device__ __forceinline__ void grad_chunk(const GradArgs& a, int64_t row, int c
     const int64_t y64 = a.targets[row];
     const float2 st = a.stats[row];
     const int y = y64 >= 0 && y64 < a.V ? (int)y64 : -1;
-    const int tid = threadIdx.x;
-    constexpr int cv = kGradThreads * kGradVecs;
+    const int tid = threadIdx.x & (NT - 1);
+    constexpr int cv = NT * kGradVecs;
     const bool careful = !(st.y > 0.f);          // (r, -S)
     const bool same = (((uint32_t)reinterpret_cast<uintptr_t>(x) ^ (uint32_t)reinterpret_cast<uintptr_t>(o)) & 15) == 0;
     const Row<T> sp(x, a.V);
@@ -721,7 +721,7 @@ __device__ __forceinline__ void grad_chunk(const GradArgs& a, int64_t row, int c
     if (y >= 0 && same) {
 #pragma unroll
         for (int u = 0; u < kGradVecs; ++u)
-            v[u] = i0 + u * kGradThreads < sp.nv ? ld_v4(xv + i0 + u * kGradThreads) : make_uint4(0, 0, 0, 0);
+            v[u] = i0 + u * NT < sp.nv ? ld_v4(xv + i0 + u * NT) : make_uint4(0, 0, 0, 0);
     }
     const float g = y >= 0 ? coef() * a.tau : 0.f;
     const float q = -g / (careful ? -st.y : st.y);
@@ -733,7 +733,7 @@ __device__ __forceinline__ void grad_chunk(const GradArgs& a, int64_t row, int c
     if (!same) {
         // the two rows cross 16-byte boundaries at different elements
         const int e1 = (ch + 1) * cv * N < a.V ? (ch + 1) * cv * N : a.V;
-        for (int e = ch * cv * N + tid; e < e1; e += kGradThreads) put(e);
+        for (int e = ch * cv * N + tid; e < e1; e += NT) put(e);
         return;
     }
     if (ch == 0) {
@@ -743,14 +743,14 @@ __device__ __forceinline__ void grad_chunk(const GradArgs& a, int64_t row, int c
     if (g == 0.f) {                              // padding, or a loss that is flat here
 #pragma unroll
         for (int u = 0; u < kGradVecs; ++u)
-            if (i0 + u * kGradThreads < sp.nv) ov[i0 + u * kGradThreads] = make_uint4(0, 0, 0, 0);
+            if (i0 + u * NT < sp.nv) ov[i0 + u * NT] = make_uint4(0, 0, 0, 0);
         return;
     }
     const int yv = y - sp.head;                  // the target among the vectors
     const int iy = yv >= 0 && yv < sp.nv * N ? yv / N : -1;
 #pragma unroll
     for (int u = 0; u < kGradVecs; ++u) {
-        const int i = i0 + u * kGradThreads;
+        const int i = i0 + u * NT;
         float f[N];
         El<T>::unpack(v[u], f);
 #pragma unroll
@@ -773,7 +773,19 @@ __global__ void __launch_bounds__(kGradThreads) k_dlogits(const GradArgs a) {
     const int row_b = blockIdx.x / (unsigned)a.chunks, ch = blockIdx.x - row_b * a.chunks;
     const int64_t row = a.M - 1 - row_b;
     const float d = a.dlogp[row];
-    grad_chunk<T>(a, row, ch, [&] { return d; });
+    grad_chunk<T, kGradThreads>(a, row, ch, [&] { return d; });
+}
+
+// The same with a row per warp, for many short rows, whose CTAs' starts took
+// most of the time (65536 x 500 bf16: 232 us, 50 by warps; 8192 x 4000: 38, 27).
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads) k_dlogits_warp(const GradArgs a) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t row = a.M - 1 - ((int64_t)blockIdx.x * (kGradThreads / 32) + (threadIdx.x >> 5));
+    if (row < 0) return;
+    const float d = a.dlogp[row];
+    for (int ch = 0; ch < a.chunks; ++ch) grad_chunk<T, 32>(a, row, ch, [&] { return d; });
 }
 
 // ---------------------------------------------------------------------------
@@ -793,13 +805,13 @@ struct PairArgs {
     float* dlogp;                // [M], or null
 };
 
-constexpr int kPairThreads = 1024, kPairCtas = 8;
-constexpr int kPairWarpTokens = 1024;            // longest pair that one warp takes
+constexpr int kPairCtas = 8;
 
 struct PairShared {
-    double red[kPairThreads / 32][4];
-    double warp_loss[kPairThreads / 32];
+    double red[32][4];
+    double warp_loss[32];
     double rank_loss[kPairCtas];
+    float2 d;                                    // gradient of a row of either sequence
     uint32_t is_long[32];
 };
 
@@ -878,33 +890,53 @@ struct PairTerms {
 };
 
 // One pair by one warp (CTA = false) or by the whole CTA; returns the pair's loss.
-template <bool CTA>
+template <bool CTA, int NT>
 __device__ __forceinline__ double do_pair(const PairArgs& a, int64_t p, PairShared& sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int id = CTA ? threadIdx.x : lane, n = CTA ? kPairThreads : 32;
+    const int id = CTA ? threadIdx.x : lane, n = CTA ? NT : 32;
     const PairRows r(a, p);
-    double t[4];
+    double t[4], loss = 0.;
     pair_sums(a, r, id, n, t);
     if (CTA) {
         if (lane == 0)
             for (int j = 0; j < 4; ++j) sh.red[warp][j] = t[j];
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) t[j] = warp_sum(sh.red[lane][j]);
-        __syncthreads();
     }
-    const PairTerms o(a, t);
-    if (id == 0) o.put_rewards(a, p);
+    float gc = 0.f, gr = 0.f;
+    if (!CTA || warp == 0) {
+        if (CTA)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) t[j] = warp_sum(lane < NT / 32 ? sh.red[lane][j] : 0.);
+        const PairTerms o(a, t);
+        loss = o.loss;
+        gc = o.gc;
+        gr = o.gr;
+        if (lane == 0) {
+            o.put_rewards(a, p);
+            if (CTA) sh.d = make_float2(gc, gr);
+        }
+    }
+    if (CTA) {
+        __syncthreads();
+        gc = sh.d.x;
+        gr = sh.d.y;
+    }
     if (a.dlogp)
-        for (int64_t i = r.s0 + id; i < r.s2; i += n) a.dlogp[i] = i < r.s1 ? o.gc : o.gr;
-    return o.loss;
+        for (int64_t i = r.s0 + id; i < r.s2; i += n) a.dlogp[i] = i < r.s1 ? gc : gr;
+    return loss;
 }
 
 // One cluster.  CTA c owns the pairs c, c + 8, ...: short ones go to its
 // warps, long ones are taken by the whole CTA, so that neither many short nor
 // few long pairs wait on one warp; the assignment and so every sum's order is
-// fixed.  Rows outside every sequence get gradient 0.
-__global__ void __launch_bounds__(kPairThreads) k_preference(const PairArgs a) {
+// fixed.  Rows outside every sequence get gradient 0.  All of it is latency:
+// with few pairs, blocks of 256 threads that find room beside the kernel before
+// them and take all but the shortest pairs whole (16 pairs of 256 rows: 2 us less
+// than blocks of 1024).
+constexpr int kPairFew = 32, kPairFewRows = 16384;
+template <int NT>
+__global__ void __launch_bounds__(NT) k_preference(const PairArgs a) {
+    constexpr int kWarpTokens = NT < 1024 ? 128 : 1024;   // longest pair that one warp takes
     __shared__ PairShared sh;
     const uint32_t rank = cluster_rank();
     cluster_arrive();
@@ -912,23 +944,22 @@ __global__ void __launch_bounds__(kPairThreads) k_preference(const PairArgs a) {
     grid_dep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     double acc = 0.;
-    for (int64_t base = 0; base * kPairCtas + rank < a.P; base += kPairThreads) {
+    for (int64_t base = 0; base * kPairCtas + rank < a.P; base += NT) {
         const int64_t mine = (base + tid) * kPairCtas + rank;
         bool lng = false;
-        if (mine < a.P) lng = (int64_t)a.cu[2 * mine + 2] - a.cu[2 * mine] > kPairWarpTokens;
+        if (mine < a.P) lng = (int64_t)a.cu[2 * mine + 2] - a.cu[2 * mine] > kWarpTokens;
         const uint32_t bits = __ballot_sync(0xffffffffu, lng);
         if (lane == 0) sh.is_long[warp] = bits;
         __syncthreads();
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < NT / 32; ++j) {
             const int64_t p = (base + 32 * j + warp) * kPairCtas + rank;
             if (p >= a.P) break;
-            if (!((sh.is_long[j] >> warp) & 1u)) acc += do_pair<false>(a, p, sh);
+            if (!((sh.is_long[j] >> warp) & 1u)) acc += do_pair<false, NT>(a, p, sh);
         }
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < NT / 32; ++j)
             for (uint32_t b = sh.is_long[j]; b; b &= b - 1) {
                 const int64_t p = (base + 32 * j + __ffs(b) - 1) * kPairCtas + rank;
-                const double l = do_pair<true>(a, p, sh);
-                if (warp == 0) acc += l;
+                acc += do_pair<true, NT>(a, p, sh);      // in warp 0
             }
         __syncthreads();
     }
@@ -936,14 +967,14 @@ __global__ void __launch_bounds__(kPairThreads) k_preference(const PairArgs a) {
         int64_t lo = a.cu[0], hi = a.cu[2 * a.P];
         lo = lo < 0 ? 0 : lo < a.M ? lo : a.M;
         hi = hi < lo ? lo : hi < a.M ? hi : a.M;
-        for (int64_t i = (int64_t)rank * kPairThreads + tid; i < lo + a.M - hi; i += kPairThreads * kPairCtas)
+        for (int64_t i = (int64_t)rank * NT + tid; i < lo + a.M - hi; i += NT * kPairCtas)
             a.dlogp[i < lo ? i : hi + i - lo] = 0.f;
     }
     if (lane == 0) sh.warp_loss[warp] = acc;
     __syncthreads();
     cluster_wait();
     if (warp == 0) {
-        const double v = warp_sum(sh.warp_loss[lane]);
+        const double v = warp_sum(lane < NT / 32 ? sh.warp_loss[lane] : 0.);
         if (lane == 0)
             asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(mapa(smem_u32(&sh.rank_loss[rank]), 0)), "d"(v)
                          : "memory");
@@ -996,7 +1027,7 @@ __global__ void __launch_bounds__(kGradThreads) k_preference_few(const FewArgs a
         return;
     }
     const int b = blockIdx.x - 1, row = b / (unsigned)a.g.chunks, ch = b - row * a.g.chunks;
-    grad_chunk<T>(a.g, row, ch, [&] {
+    grad_chunk<T, kGradThreads>(a.g, row, ch, [&] {
         // sequences that begin at or before the row; the row is in the last of them
         int seq = -1;
         for (int64_t i = 0; i <= 2 * a.p.P; i += kGradThreads)
@@ -1195,18 +1226,27 @@ __global__ void __launch_bounds__(kBlockThreads) k_policy_short(const PolicyArgs
     }
 }
 
-constexpr int kFinishThreads = 1024;
+constexpr int kFinishThreads = 256, kFinishCtas = 8;
 
-// stats[j] = sum over rows of component j, fp64 in a fixed order
-__global__ void __launch_bounds__(kFinishThreads) k_policy_finish(const float4* part, int64_t M, float* stats) {
-    __shared__ double s[kFinishThreads / 32][4];
+struct FinishSums {
+    const float4* part;          // [M]
+    int64_t M;
+    float* stats;                // [4]
+};
+
+// stats[j] = sum over rows of component j, fp64 in a fixed order, by one
+// cluster of blocks small enough to find room beside the kernel before it.
+__global__ void __launch_bounds__(kFinishThreads) k_policy_finish(const FinishSums a) {
+    __shared__ double s[kFinishThreads / 32][4], total[kFinishCtas][4];
+    const uint32_t rank = cluster_rank(), z = cluster_size();
+    if (z > 1) cluster_arrive();
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     double t[4] = {0., 0., 0., 0.};
 #pragma unroll 4
-    for (int64_t i = tid; i < M; i += kFinishThreads) {
-        const float4 p = part[i];
+    for (int64_t i = rank * kFinishThreads + tid; i < a.M; i += z * kFinishThreads) {
+        const float4 p = a.part[i];
         t[0] += p.x; t[1] += p.y; t[2] += p.z; t[3] += p.w;
     }
 #pragma unroll
@@ -1215,9 +1255,21 @@ __global__ void __launch_bounds__(kFinishThreads) k_policy_finish(const float4* 
         if (lane == 0) s[warp][j] = t[j];
     }
     __syncthreads();
-    if (warp < 4) {
-        const double v = warp_sum(s[lane][warp]);
-        if (lane == 0) stats[warp] = (float)v;
+    if (z > 1) cluster_wait();                   // every CTA of the cluster runs
+    if (tid < 4) {
+        double v = 0.;
+        for (int w = 0; w < kFinishThreads / 32; ++w) v += s[w][tid];
+        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(mapa(smem_u32(&total[rank][tid]), 0)), "d"(v) : "memory");
+    }
+    if (z > 1) {
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+    }
+    if (rank == 0 && tid < 4) {
+        double v = 0.;
+        for (uint32_t q = 0; q < z; ++q) v += total[q][tid];
+        a.stats[tid] = (float)v;
     }
 }
 

@@ -1716,8 +1716,18 @@ int preference_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t
                    : launch_rows<loss::FewArgs>(loss::k_preference_few<uint16_t>, M * chunks + 1, 1, loss::kGradThreads, st,
                                                 fa);
     }
-    rc = launch_rows<loss::PairArgs>(loss::k_preference, 1, loss::kPairCtas, loss::kPairThreads, st, a);
+    rc = P <= loss::kPairFew && M <= loss::kPairFewRows ? launch_rows<loss::PairArgs>(loss::k_preference<256>, 1, loss::kPairCtas, 256, st, a)
+                             : launch_rows<loss::PairArgs>(loss::k_preference<1024>, 1, loss::kPairCtas, 1024, st, a);
     if (rc != QLORA_OK || !dlogits) return rc;
+    // a row per warp where that gives every SM two CTAs, or takes one pass
+    const int64_t nv = cdiv(V, N);
+    if (nv <= 32 * loss::kGradVecs || (nv <= 640 && M >= 2 * (int64_t)sms * (loss::kGradThreads / 32))) {
+        g.chunks = (int)cdiv(nv, 32 * (int64_t)loss::kGradVecs);
+        const int64_t ctas = cdiv(M, (int64_t)loss::kGradThreads / 32);
+        return dtype == QLORA_LOGITS_FP32
+                   ? launch_rows<loss::GradArgs>(loss::k_dlogits_warp<float>, ctas, 1, loss::kGradThreads, st, g)
+                   : launch_rows<loss::GradArgs>(loss::k_dlogits_warp<uint16_t>, ctas, 1, loss::kGradThreads, st, g);
+    }
     return dtype == QLORA_LOGITS_FP32
                ? launch_rows<loss::GradArgs>(loss::k_dlogits<float>, M * chunks, 1, loss::kGradThreads, st, g)
                : launch_rows<loss::GradArgs>(loss::k_dlogits<uint16_t>, M * chunks, 1, loss::kGradThreads, st, g);
@@ -1754,8 +1764,9 @@ int policy_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld,
     a.logp = logp; a.part = static_cast<float4*>(ws); a.out = dlogits; a.ldo = ldd;
     rc = dtype == QLORA_LOGITS_FP32 ? launch_policy<float>(a, sms, st) : launch_policy<uint16_t>(a, sms, st);
     if (rc != QLORA_OK) return rc;
-    return launch_pdl(loss::k_policy_finish, dim3(1), dim3(loss::kFinishThreads), 0, st, (const float4*)a.part, M,
-                      stats);
+    const loss::FinishSums f{a.part, M, stats};
+    return launch_rows<loss::FinishSums>(loss::k_policy_finish, 1, M <= loss::kFinishThreads ? 1 : loss::kFinishCtas,
+                                         loss::kFinishThreads, st, f);
 }
 
 
