@@ -698,10 +698,10 @@ struct GradArgs {
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;                     // 16-byte vectors per thread
 
-// One chunk of NT * kGradVecs vectors of row `row` by NT threads: coef() is called
+// One chunk of NT * VECS vectors of row `row` by NT threads: coef() is called
 // once by every thread, with the chunk's loads under way, and gives
 // d loss / d logp of the row (a row without a target is zeroed without it).
-template <typename T, int NT, typename Coef>
+template <typename T, int NT, int VECS, typename Coef>
 __device__ __forceinline__ void grad_chunk(const GradArgs& a, int64_t row, int ch, Coef coef) {
     constexpr int N = El<T>::N;
     const T* x = static_cast<const T*>(a.logits) + row * a.ld;
@@ -710,17 +710,17 @@ __device__ __forceinline__ void grad_chunk(const GradArgs& a, int64_t row, int c
     const float2 st = a.stats[row];
     const int y = y64 >= 0 && y64 < a.V ? (int)y64 : -1;
     const int tid = threadIdx.x & (NT - 1);
-    constexpr int cv = NT * kGradVecs;
+    constexpr int cv = NT * VECS;
     const bool careful = !(st.y > 0.f);          // (r, -S)
     const bool same = (((uint32_t)reinterpret_cast<uintptr_t>(x) ^ (uint32_t)reinterpret_cast<uintptr_t>(o)) & 15) == 0;
     const Row<T> sp(x, a.V);
     const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
     uint4* ov = reinterpret_cast<uint4*>(o + sp.head);
     const int i0 = ch * cv + tid;
-    uint4 v[kGradVecs];
+    uint4 v[VECS];
     if (y >= 0 && same) {
 #pragma unroll
-        for (int u = 0; u < kGradVecs; ++u)
+        for (int u = 0; u < VECS; ++u)
             v[u] = i0 + u * NT < sp.nv ? ld_v4(xv + i0 + u * NT) : make_uint4(0, 0, 0, 0);
     }
     const float g = y >= 0 ? coef() * a.tau : 0.f;
@@ -742,14 +742,14 @@ __device__ __forceinline__ void grad_chunk(const GradArgs& a, int64_t row, int c
     }
     if (g == 0.f) {                              // padding, or a loss that is flat here
 #pragma unroll
-        for (int u = 0; u < kGradVecs; ++u)
+        for (int u = 0; u < VECS; ++u)
             if (i0 + u * NT < sp.nv) ov[i0 + u * NT] = make_uint4(0, 0, 0, 0);
         return;
     }
     const int yv = y - sp.head;                  // the target among the vectors
     const int iy = yv >= 0 && yv < sp.nv * N ? yv / N : -1;
 #pragma unroll
-    for (int u = 0; u < kGradVecs; ++u) {
+    for (int u = 0; u < VECS; ++u) {
         const int i = i0 + u * NT;
         float f[N];
         El<T>::unpack(v[u], f);
@@ -766,14 +766,14 @@ __device__ __forceinline__ void grad_chunk(const GradArgs& a, int64_t row, int c
 
 // One chunk per CTA, the last rows first: those are what the forward pass has
 // left in L2.
-template <typename T>
+template <typename T, int VECS>
 __global__ void __launch_bounds__(kGradThreads) k_dlogits(const GradArgs a) {
     grid_dep_wait();
     grid_dep_launch();
     const int row_b = blockIdx.x / (unsigned)a.chunks, ch = blockIdx.x - row_b * a.chunks;
     const int64_t row = a.M - 1 - row_b;
     const float d = a.dlogp[row];
-    grad_chunk<T, kGradThreads>(a, row, ch, [&] { return d; });
+    grad_chunk<T, kGradThreads, VECS>(a, row, ch, [&] { return d; });
 }
 
 // The same with a row per warp, for many short rows, whose CTAs' starts took
@@ -785,7 +785,7 @@ __global__ void __launch_bounds__(kGradThreads) k_dlogits_warp(const GradArgs a)
     const int64_t row = a.M - 1 - ((int64_t)blockIdx.x * (kGradThreads / 32) + (threadIdx.x >> 5));
     if (row < 0) return;
     const float d = a.dlogp[row];
-    for (int ch = 0; ch < a.chunks; ++ch) grad_chunk<T, 32>(a, row, ch, [&] { return d; });
+    for (int ch = 0; ch < a.chunks; ++ch) grad_chunk<T, 32, kGradVecs>(a, row, ch, [&] { return d; });
 }
 
 // ---------------------------------------------------------------------------
@@ -1027,7 +1027,7 @@ __global__ void __launch_bounds__(kGradThreads) k_preference_few(const FewArgs a
         return;
     }
     const int b = blockIdx.x - 1, row = b / (unsigned)a.g.chunks, ch = b - row * a.g.chunks;
-    grad_chunk<T, kGradThreads>(a.g, row, ch, [&] {
+    grad_chunk<T, kGradThreads, kGradVecs>(a.g, row, ch, [&] {
         // sequences that begin at or before the row; the row is in the last of them
         int seq = -1;
         for (int64_t i = 0; i <= 2 * a.p.P; i += kGradThreads)

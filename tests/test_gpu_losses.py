@@ -226,6 +226,20 @@ LARGE = [(2100, 16400, 7, "bf16", 0, 0.1, False, 16400, 0), (530, 65537, 3, "bf1
          (4100, 4100, 40, "fp32", 1, 0.0, False, 4103, 1), (600, 32001, 60, "bf16", 0, 0.0, True, 32010, 3)]
 
 
+# many short rows (a warp each), and rows around the lengths that take one vector a thread or one chunk more
+WIDTHS = [(2500, 600, 5, "bf16", 0, 0.0, False, 603, 1), (2500, 5120, 33, "bf16", 1, 0.0, True, 5120, 0),
+          (2500, 2559, 33, "fp32", 0, 0.1, False, 2561, 1), (700, 513, 40, "fp32", 2, 0.0, True, 513, 0),
+          (600, 5135, 33, "bf16", 0, 0.0, False, 5135, 0), (600, 8200, 33, "bf16", 0, 0.1, False, 8200, 0),
+          (600, 12288, 33, "bf16", 2, 0.0, True, 12290, 3), (600, 12297, 33, "bf16", 0, 0.0, False, 12297, 0),
+          (600, 6145, 33, "fp32", 1, 0.0, False, 6146, 1)]
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("M,V,P,dtype,kind,eps,average,ld,off", WIDTHS)
+def test_preference_rows_of_every_width(M, V, P, dtype, kind, eps, average, ld, off, inplace):
+    _run_preference(M + V, M, V, P, dtype, kind, eps, 0.0, average, ld=ld, off=off, beta=0.02, inplace=inplace)
+
+
 @pytest.mark.parametrize("inplace", [False, True])
 @pytest.mark.parametrize("M,V,P,dtype,kind,eps,average,ld,off", LARGE)
 def test_preference_large(M, V, P, dtype, kind, eps, average, ld, off, inplace):
