@@ -268,6 +268,7 @@ struct BlockShared {
     KS rank[kMaxZ];                              // written by the CTAs of the cluster
     RowShared careful;
     float4 row;                                  // what warp 0 made of the row
+    float at_y;
     unsigned long long xbar;                     // what the cluster's CTAs send
     int abort;
 };
@@ -339,13 +340,21 @@ __device__ __forceinline__ KS sum_pass(const uint4 (&v)[NV], float x1, float c, 
     return acc;
 }
 
-// -g p = q ex2(c l - k); g is added at the target by the thread that has just written there.
+// An element's exponent in the gradient; c_lo would be lost in a bf16 result.
+template <typename T>
+__device__ __forceinline__ float grad_exp(float l, float c, float c_lo, float k) {
+    const float t = fmaf(l, c, -k);
+    return sizeof(T) == 4 ? fmaf(l, c_lo, t) : t;
+}
+
+// -g p = q ex2(c l - k); the target's element is at_y, which the thread that has just written there writes:
+// g (1 - p) from the log-probability, so that nothing cancels where p is almost 1.
 template <typename T, int NT, int NV>
-__device__ __forceinline__ void grad_pass(uint4 (&v)[NV], float x1, float ly, T* o, const Row<T>& sp, int v0, int nv,
-                                          int e1, int y, float c, float k, float q, float g) {
+__device__ __forceinline__ void grad_pass(uint4 (&v)[NV], float x1, float at_y, T* o, const Row<T>& sp, int v0, int nv,
+                                          int e1, int y, float c, float c_lo, float k, float q) {
     constexpr int N = El<T>::N;
     const int tid = threadIdx.x & (NT - 1);
-    const f32x2 c2 = pk2(c, c), k2 = pk2(-k, -k), q2 = pk2(q, q);
+    const f32x2 c2 = pk2(c, c), l2 = pk2(c_lo, c_lo), k2 = pk2(-k, -k), q2 = pk2(q, q);
     uint4* ov = reinterpret_cast<uint4*>(o + sp.head + v0 * N);
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
@@ -355,15 +364,16 @@ __device__ __forceinline__ void grad_pass(uint4 (&v)[NV], float x1, float ly, T*
 #pragma unroll
         for (int j = 0; j < Pairs<T>::N; ++j) {
             float t0, t1;
-            un2(fma2(Pairs<T>::get(v[u], j), c2, k2), t0, t1);
+            const f32x2 p = Pairs<T>::get(v[u], j), t = fma2(p, c2, k2);
+            un2(sizeof(T) == 4 ? fma2(p, l2, t) : t, t0, t1);
             un2(mul2(pk2(ex2(t0), ex2(t1)), q2), f[2 * j], f[2 * j + 1]);
         }
         if (tid + u * NT < nv) ov[tid + u * NT] = El<T>::pack(f);
     }
-    if (e1 >= 0) o[e1] = El<T>::put(q * ex2(fmaf(x1, c, -k)));
+    if (e1 >= 0) o[e1] = El<T>::put(q * ex2(grad_exp<T>(x1, c, c_lo, k)));
     const int yv = y - sp.head - v0 * N;                  // the target among this CTA's vectors
     const bool mine = yv >= 0 && yv < nv * N ? ((yv / N) & (NT - 1)) == tid : e1 == y;
-    if (mine) o[y] = El<T>::put(fmaf(q, ex2(fmaf(ly, c, -k)), g));
+    if (mine) o[y] = El<T>::put(at_y);
 }
 
 // The careful form of one row, read again from memory (rows out of k's range:
@@ -412,8 +422,8 @@ __device__ __forceinline__ void zero_row(T* o, int V, int v0, int v1, uint32_t r
 // gradient row whose 16-byte boundaries are not the logits' (q = -g / S, and
 // k as in the vector path, whose results these equal bit for bit).
 template <typename T>
-__device__ __noinline__ void scalar_grad(const T* x, T* o, int V, int y, int v0, int v1, float c, bool careful, MS ms,
-                                         float k, float q, float g, uint32_t rank) {
+__device__ __noinline__ void scalar_grad(const T* x, T* o, int V, int y, int v0, int v1, float c, float c_lo, bool careful,
+                                         MS ms, float k, float q, float g, float at_y, uint32_t rank) {
     const Row<T> sp(x, V);
     auto put = [&](int e) {
         const float l = El<T>::get(x[e]);
@@ -421,8 +431,8 @@ __device__ __noinline__ void scalar_grad(const T* x, T* o, int V, int y, int v0,
             const float p = ex2((l - ref_of(ms.m)) * c) / ms.s;
             o[e] = El<T>::put(e == y ? g - g * p : -g * p);
         } else {
-            const float p = ex2(fmaf(l, c, -k));
-            o[e] = El<T>::put(e == y ? fmaf(q, p, g) : q * p);
+            const float p = ex2(grad_exp<T>(l, c, c_lo, k));
+            o[e] = El<T>::put(e == y ? at_y : q * p);
         }
     };
     for (int e = sp.head + v0 * El<T>::N + threadIdx.x; e < sp.head + v1 * El<T>::N; e += blockDim.x) put(e);
@@ -686,8 +696,9 @@ struct GradArgs {
     const void* logits;
     int64_t M, ld;
     int V;
-    float tau, c;
+    float tau, c, c_lo;
     const int64_t* targets;
+    const double* lpd;           // [M] of k_token_logprob
     const float2* stats;         // [M] of k_token_logprob
     const float* dlogp;          // [M] (not used where the target is outside [0, V))
     void* out;                   // may be the logits themselves (ldo == ld)
@@ -725,10 +736,11 @@ __device__ __forceinline__ void grad_chunk(const GradArgs& a, int64_t row, int c
     }
     const float g = y >= 0 ? coef() * a.tau : 0.f;
     const float q = -g / (careful ? -st.y : st.y);
-    auto one = [&](float l) { return q * ex2(careful ? (l - st.x) * a.c : fmaf(l, a.c, -st.x)); };
+    auto one = [&](float l) { return q * ex2(careful ? (l - st.x) * a.c : grad_exp<T>(l, a.c, a.c_lo, st.x)); };
+    auto at_y = [&] { return -g * expm1f((float)a.lpd[row]); };
     auto put = [&](int e) {
         const float f = g == 0.f ? 0.f : one(El<T>::get(x[e]));
-        o[e] = El<T>::put(g != 0.f && e == y ? f + g : f);
+        o[e] = El<T>::put(g != 0.f && e == y ? at_y() : f);
     };
     if (!same) {
         // the two rows cross 16-byte boundaries at different elements
@@ -758,7 +770,7 @@ __device__ __forceinline__ void grad_chunk(const GradArgs& a, int64_t row, int c
         if (i == iy) {
 #pragma unroll
             for (int j = 0; j < N; ++j)
-                if (j == (yv & (N - 1))) f[j] += g;
+                if (j == (yv & (N - 1))) f[j] = at_y();
         }
         if (i < sp.nv) ov[i] = El<T>::pack(f);
     }
@@ -1070,17 +1082,54 @@ struct PolicyArgs {
     int64_t ldo;
 };
 
+// A log-probability in base 2, unevaluated sum of two fp32.  The ratio is the
+// exponential of a difference of two log-probabilities of about -10, whose
+// fp32 rounding alone would be 5e-7 of the gradient of the row.
+struct Lp2 {
+    float hi, lo;
+};
+
+// c l_y + c_lo l_y - k - log2 S, with S = 2^e m, m in [1/2, 1)  and the integers taken off exactly.
+__device__ __forceinline__ Lp2 lp2_of(float ly, KS t, float c, float c_lo) {
+    const int b = (int)(__float_as_uint(t.s) >> 23) - 126;        // in_range: not subnormal but for S < 2^-126
+    const bool normal = b > -126;
+    const float m = normal ? __uint_as_float((__float_as_uint(t.s) & 0x007fffffu) | 0x3f000000u) : t.s;
+    const float K = t.k + (normal ? (float)b : 0.f), p = ly * c, s = p - K, v = s - p;
+    const float lo = fmaf(ly, c, -p) + ((p - (s - v)) + (-K - v)) + fmaf(ly, c_lo, -log2f(m)) -
+                     (float)kEx2Low * kLog2e;
+    Lp2 r{s, fabsf(s) < INFINITY ? lo : 0.f};
+    if (r.hi + r.lo > 0.f) r = Lp2{0.f, 0.f};
+    return r;
+}
+__device__ __forceinline__ Lp2 lp2_of(double lp) {
+    const double d = lp * 1.4426950408889634074;
+    const float hi = (float)d;
+    return Lp2{hi, fabsf(hi) < INFINITY ? (float)(d - (double)hi) : 0.f};
+}
+
+constexpr float kLog2eLo = (float)(1.4426950408889634074 - (double)kLog2e), kLn2Lo = (float)(0.69314718055994530942 - (double)kLn2);
+
+// lp - x in base 2, x a natural log-probability
+__device__ __forceinline__ float lp2_minus(Lp2 lp, float x) {
+    const float h = x * kLog2e, e = fmaf(x, kLog2eLo, fmaf(x, kLog2e, -h));
+    return (lp.hi - h) + (lp.lo - (fabsf(h) < INFINITY ? e : 0.f));
+}
+
+// 1 - p = -(e^lp - 1)
+__device__ __forceinline__ float lp2_rest(Lp2 lp) { return -expm1f((lp.hi + lp.lo) * kLn2); }
+
 // The row's loss terms (written by the thread that is told to) and d loss /
 // d logit scale: what multiplies 1[v = y] - p_v.
-__device__ __forceinline__ float policy_row(const PolicyArgs& a, int row, float lp, float A, float w, float old,
+__device__ __forceinline__ float policy_row(const PolicyArgs& a, int row, Lp2 lp, float A, float w, float old,
                                             float ref, bool put) {
-    const float rho = a.old_logp ? expf(lp - old) : 1.f;
+    const float rho = a.old_logp ? exp2f(lp2_minus(lp, old)) : 1.f;
     const float free_ = rho * A, held = fminf(fmaxf(rho, a.lo), a.hi) * A;
     const bool clipped = held < free_;
-    const float d = a.ref_logp ? ref - lp : 0.f, em = expm1f(d);
+    const float d = a.ref_logp ? -lp2_minus(lp, ref) * kLn2 : 0.f, em = expm1f(d);
     if (put) {
         const float pol = -(clipped ? held : free_), kl = em - d;
-        a.logp[row] = lp;
+        const float r = lp.hi * kLn2;
+        a.logp[row] = fabsf(r) < INFINITY ? r + (fmaf(lp.hi, kLn2, -r) + fmaf(lp.hi, kLn2Lo, lp.lo * kLn2)) : r;
         a.part[row] = make_float4(w * (pol + a.kl * kl), w * pol, w * kl, clipped ? w : 0.f);
     }
     return w * ((clipped ? 0.f : -free_) - a.kl * em) * a.grad_scale * a.tau;
@@ -1146,10 +1195,14 @@ __global__ void __launch_bounds__(kBlockThreads) k_policy_block(const PolicyArgs
     t = block_total(t, sh, rank, z);
     if (tid < 32) {
         // the loss of the row and its derivative, by one warp
-        const float lp = (fmaf(ly, a.c_lo, fmaf(ly, a.c, -t.k)) - log2f(t.s)) * kLn2;
         const bool fine = in_range(t.s);
-        const float g = fine ? policy_row(a, row, lp > 0.f ? 0.f : lp, A, w, old, ref, rank == 0 && tid == 0) : 0.f;
-        if (tid == 0) sh.row = make_float4(t.k, -g / t.s, g, fine ? 0.f : 1.f);
+        const Lp2 lp = lp2_of(ly, t, a.c, a.c_lo);
+        const float g = fine ? policy_row(a, row, lp, A, w, old, ref, rank == 0 && tid == 0) : 0.f;
+        const float at_y = g * lp2_rest(lp);
+        if (tid == 0) {
+            sh.row = make_float4(t.k, -g / t.s, g, fine ? 0.f : 1.f);
+            sh.at_y = at_y;
+        }
     }
     __syncthreads();
     const float4 rv = sh.row;
@@ -1160,16 +1213,16 @@ __global__ void __launch_bounds__(kBlockThreads) k_policy_block(const PolicyArgs
     if (careful) {
         // out of k's range, NaN, or nothing above -inf
         ms = careful_total(x, V, v0, v1, a.c, sh, rank, z);
-        g = policy_row(a, row, (float)logp_of(ly, ms, a.tau), A, w, old, ref, rank == 0 && tid == 0);
+        g = policy_row(a, row, lp2_of(logp_of(ly, ms, a.tau)), A, w, old, ref, rank == 0 && tid == 0);
     }
     if (a.out == nullptr) return;
     const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
     if (g == 0.f) {                                       // a loss that is flat here
         zero_row(o, V, v0, v1, rank);
     } else if (careful || !same) {
-        scalar_grad(x, o, V, y, v0, v1, a.c, careful, ms, k, q, g, rank);
+        scalar_grad(x, o, V, y, v0, v1, a.c, a.c_lo, careful, ms, k, q, g, sh.at_y, rank);
     } else {
-        grad_pass<T, NT, NV>(v, x1, ly, o, sp, v0, nv, e1, y, a.c, k, q, g);
+        grad_pass<T, NT, NV>(v, x1, sh.at_y, o, sp, v0, nv, e1, y, a.c, a.c_lo, k, q);
     }
 }
 
@@ -1201,13 +1254,12 @@ __global__ void __launch_bounds__(kBlockThreads) k_policy_short(const PolicyArgs
     const KS t = r.total(a.c, a.c_lo, sh);
     const bool careful = !in_range(t.s);
     MS ms{0.f, 1.f};
-    float lp;
+    Lp2 lp;
     if (careful) {
         ms = ShortRow<T, NT, NV>::careful(x, V, a.c, sh);
-        lp = (float)logp_of(ly, ms, a.tau);
+        lp = lp2_of(logp_of(ly, ms, a.tau));
     } else {
-        lp = (fmaf(ly, a.c_lo, fmaf(ly, a.c, -t.k)) - log2f(t.s)) * kLn2;
-        lp = lp > 0.f ? 0.f : lp;
+        lp = lp2_of(ly, t, a.c, a.c_lo);
     }
     const float g = policy_row(a, (int)row, lp, A, w, old, ref, id == 0);
     if (a.out == nullptr) return;
@@ -1218,11 +1270,11 @@ __global__ void __launch_bounds__(kBlockThreads) k_policy_short(const PolicyArgs
     } else if (careful || !same) {
         for (int e = id; e < V; e += NT) {
             const float l = El<T>::get(x[e]);
-            const float p = ex2(careful ? (l - ref_of(ms.m)) * a.c : fmaf(l, a.c, -k));
-            o[e] = El<T>::put(e == y ? fmaf(q, p, g) : q * p);
+            const float p = ex2(careful ? (l - ref_of(ms.m)) * a.c : grad_exp<T>(l, a.c, a.c_lo, k));
+            o[e] = El<T>::put(e == y ? g * lp2_rest(lp) : q * p);
         }
     } else {
-        grad_pass<T, NT, NV>(r.v, r.x1, ly, o, r.sp, 0, r.sp.nv, r.e1, y, a.c, k, q, g);
+        grad_pass<T, NT, NV>(r.v, r.x1, g * lp2_rest(lp), o, r.sp, 0, r.sp.nv, r.e1, y, a.c, a.c_lo, k, q);
     }
 }
 

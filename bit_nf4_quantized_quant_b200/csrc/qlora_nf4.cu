@@ -1719,9 +1719,8 @@ int preference_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t
     a.grad_scale = grad_scale; a.loss = loss; a.rewards = rewards; a.dlogp = dlogits ? dlogp : nullptr;
     loss::GradArgs g{};
     g.logits = logits; g.M = M; g.V = (int)V; g.ld = ld; g.tau = logit_scale;
-    float c_lo;
-    split_c(logit_scale, &g.c, &c_lo);
-    g.targets = targets; g.stats = stats; g.dlogp = dlogp; g.out = dlogits; g.ldo = ldd; g.chunks = (int)chunks;
+    split_c(logit_scale, &g.c, &g.c_lo);
+    g.targets = targets; g.lpd = lpd; g.stats = stats; g.dlogp = dlogp; g.out = dlogits; g.ldo = ldd; g.chunks = (int)chunks;
     if (dlogits && M <= loss::kFewRows && P <= loss::kFewPairs) {
         const loss::FewArgs fa{a, g};
         return dtype == QLORA_LOGITS_FP32
