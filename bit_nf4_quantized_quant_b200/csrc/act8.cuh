@@ -21,7 +21,8 @@
 // holds values 8l..8l+7, so loads and stores of every instruction are
 // contiguous across the warp and the block maximum is two shuffles over 4
 // lanes on packed 16-bit integers (the magnitude order of bf16 is the order
-// of its bit patterns).  Launched programmatically: a kernel waits for the one
+// of its bit patterns).  4096 x 28672 int8 (356 MB either way): 59 us to quantize,
+// 53 us back, of 54 at the copy rate.  Launched programmatically: a kernel waits for the one
 // before it before it reads anything.
 #pragma once
 #include "common.cuh"
