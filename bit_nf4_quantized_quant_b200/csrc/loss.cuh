@@ -1125,7 +1125,8 @@ __device__ __forceinline__ Lp2 lp2_of(double lp) {
     return Lp2{hi, fabsf(hi) < INFINITY ? (float)(d - (double)hi) : 0.f};
 }
 
-constexpr float kLog2eLo = (float)(1.4426950408889634074 - (double)kLog2e), kLn2Lo = (float)(0.69314718055994530942 - (double)kLn2);
+constexpr float kLog2eLo = (float)(1.4426950408889634074 - (double)kLog2e);
+constexpr float kLn2Lo = (float)(0.69314718055994530942 - (double)kLn2);
 
 // lp - x in base 2, x a natural log-probability
 __device__ __forceinline__ float lp2_minus(Lp2 lp, float x) {

@@ -1728,8 +1728,9 @@ int preference_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t
                    : launch_rows<loss::FewArgs>(loss::k_preference_few<uint16_t>, M * chunks + 1, 1, loss::kGradThreads, st,
                                                 fa);
     }
-    rc = P <= loss::kPairFew && M <= loss::kPairFewRows ? launch_rows<loss::PairArgs>(loss::k_preference<256>, 1, loss::kPairCtas, 256, st, a)
-                             : launch_rows<loss::PairArgs>(loss::k_preference<1024>, 1, loss::kPairCtas, 1024, st, a);
+    rc = P <= loss::kPairFew && M <= loss::kPairFewRows
+             ? launch_rows<loss::PairArgs>(loss::k_preference<256>, 1, loss::kPairCtas, 256, st, a)
+             : launch_rows<loss::PairArgs>(loss::k_preference<1024>, 1, loss::kPairCtas, 1024, st, a);
     if (rc != QLORA_OK || !dlogits) return rc;
     // a row per warp where that gives every SM two CTAs, or takes one pass
     const int64_t nv = cdiv(V, N);
