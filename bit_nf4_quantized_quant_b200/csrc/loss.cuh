@@ -7,9 +7,10 @@
 //   d logp_m / d l_v = tau (1[v = y] - p_v),   p_v = exp(tau (l_v - r)) / S
 // evaluated in base 2, with c = tau log2 e: ex2(c l - k) with an integer k near
 // c r, one fused multiply-add an element; S is then s 2^k.  A row whose s comes
-// out as 0, infinite or NaN is done again in the careful form above, l - r formed
-// before the product: a row of equal lowest values is uniform, -inf entries give
-// exactly 0, and r = 0 stands in where nothing is above -inf.  Sums are fp32 per
+// out as 0, infinite or NaN, or whose k is beyond +-2^20, is done again in the
+// careful form above, l - r formed before the product: a row of equal lowest
+// values is uniform, -inf entries give exactly 0, and r = 0 stands in where
+// nothing is above -inf.  Sums are fp32 per
 // thread, warp and block; sums over the tokens of a sequence and over rows are
 // fp64 in a fixed order.
 //
@@ -183,12 +184,15 @@ __device__ __forceinline__ MS row_total(MS v, float c, RowShared& sh, uint32_t r
 // t = c l - k is one rounding: c l - k in one fused multiply-add, to which the
 // rest c_lo of c (c + c_lo is tau log2 e to 48 bits) is added.  Logits beyond
 // +-2^100 leave the range that k is clamped to; a row's sum is then 0 or
-// infinite, and the row is done again in the careful form above.
+// infinite, and the row is done again in the careful form above.  So is a row
+// whose k is beyond +-kFar: from there on c l is no longer known to a small part
+// of 1 (a step of fp32 at 2^20 is 1/8, the 48 bits of c + c_lo end at 2^-28), and
+// with it neither k + log2 s nor p.
 struct __align__(8) KS {
     float k, s;
 };
 
-constexpr float kTop = 0x1p100f;
+constexpr float kTop = 0x1p100f, kFar = 0x1p20f;
 
 __device__ __forceinline__ float round_k(float m, float c) { return ceilf(fminf(fmaxf(m * c, -kTop), kTop)); }
 
@@ -399,8 +403,8 @@ __device__ __forceinline__ void grad_pass(uint4 (&v)[NV], float x1, float at_y, 
     if (mine) o[y] = El<T>::put(at_y);
 }
 
-// The careful form of one row, read again from memory (rows out of k's range:
-// rare): this CTA's vectors [v0, v1) and, in rank 0, the head and the tail.
+// The careful form of one row, read again from memory (rows with k beyond kFar
+// or a sum out of range: rare): this CTA's vectors [v0, v1) and, in rank 0, the head and the tail.
 template <typename T>
 __device__ __noinline__ MS careful_total(const T* x, int V, int v0, int v1, float c, BlockShared& sh,
                                          uint32_t rank, uint32_t z) {
@@ -568,7 +572,8 @@ __device__ __forceinline__ double logp_of(float ly, MS t, float tau) {
     return lp > 0. ? 0. : lp;
 }
 
-__device__ __forceinline__ bool in_range(float S) { return S > 0.f && S < INFINITY; }
+// Whether a row's sum stands; the row is done again in the careful form if not.
+__device__ __forceinline__ bool in_range(KS t) { return t.s > 0.f && t.s < INFINITY && fabsf(t.k) <= kFar; }
 
 __device__ __forceinline__ void put_logp(const RowArgs& a, int64_t row, double lp, float2 st) {
     a.logp[row] = (float)lp;
@@ -594,7 +599,7 @@ __global__ void __launch_bounds__(kBlockThreads) k_token_logprob_short(const Row
     const T* x = static_cast<const T*>(a.logits) + row * a.ld;
     const float ly = El<T>::get(x[y]);
     const KS t = ShortRow<T, NT, NV>(x, a.V).total(a.c, a.c_lo, sh);
-    if (in_range(t.s)) {
+    if (in_range(t)) {
         if (first) put_logp(a, row, logp_of(ly, t, a.c, a.c_lo), make_float2(t.k, t.s));
     } else {
         const MS ms = ShortRow<T, NT, NV>::careful(x, a.V, a.c, sh);
@@ -697,7 +702,7 @@ __global__ void __launch_bounds__(kRowThreads) k_token_logprob(const RowArgs a) 
     acc.s = sa + sb;
     if (z > 1) cluster_wait();                   // every CTA of the cluster runs
     const KS t = block_total(acc, sh, rank, z);
-    if (tid == 0) sh.row.x = in_range(t.s) ? 1.f : 0.f;
+    if (tid == 0) sh.row.x = in_range(t) ? 1.f : 0.f;
     __syncthreads();
     if (sh.row.x != 0.f) {
         if (rank == 0 && tid == 0) put_logp(a, row, logp_of(ly, t, a.c, a.c_lo), make_float2(t.k, t.s));
@@ -1107,7 +1112,8 @@ struct Lp2 {
     float hi, lo;
 };
 
-// c l_y + c_lo l_y - k - log2 S, with S = 2^e m, m in [1/2, 1)  and the integers taken off exactly.
+// c l_y + c_lo l_y - k - log2 S, with S = 2^e m, m in [1/2, 1)  and the integers taken off exactly
+// (in_range: |k| <= 2^20, so that k + e is a whole number that fp32 holds).
 __device__ __forceinline__ Lp2 lp2_of(float ly, KS t, float c, float c_lo) {
     const int b = (int)(__float_as_uint(t.s) >> 23) - 126;        // in_range: not subnormal but for S < 2^-126
     const bool normal = b > -126;
@@ -1216,7 +1222,7 @@ __global__ void __launch_bounds__(kBlockThreads) k_policy_block(const PolicyArgs
     t = block_total(t, sh, rank, z);
     if (tid < 32) {
         // the loss of the row and its derivative, by one warp
-        const bool fine = in_range(t.s);
+        const bool fine = in_range(t);
         const Lp2 lp = lp2_of(ly, t, a.c, a.c_lo);
         const float g = fine ? policy_row(a, row, lp, A, w, old, ref, rank == 0 && tid == 0) : 0.f;
         const float at_y = g * lp2_rest(lp);
@@ -1232,7 +1238,7 @@ __global__ void __launch_bounds__(kBlockThreads) k_policy_block(const PolicyArgs
     const bool careful = rv.w != 0.f;
     MS ms{0.f, 1.f};
     if (careful) {
-        // out of k's range, NaN, or nothing above -inf
+        // far from 0, out of k's range, NaN, or nothing above -inf
         ms = careful_total(x, V, v0, v1, a.c, sh, rank, z);
         g = policy_row(a, row, lp2_of(logp_of(ly, ms, a.tau)), A, w, old, ref, rank == 0 && tid == 0);
     }
@@ -1273,7 +1279,7 @@ __global__ void __launch_bounds__(kBlockThreads) k_policy_short(const PolicyArgs
     const float old = a.old_logp ? a.old_logp[row] : 0.f, ref = a.ref_logp ? a.ref_logp[row] : 0.f;
     ShortRow<T, NT, NV> r(x, V);
     const KS t = r.total(a.c, a.c_lo, sh);
-    const bool careful = !in_range(t.s);
+    const bool careful = !in_range(t);
     MS ms{0.f, 1.f};
     Lp2 lp;
     if (careful) {

@@ -1,0 +1,77 @@
+"""The losses on logits where their arithmetic is at its limits: rows far from 0, exponentials and sums out of range.
+
+Tolerances, from the kernels' fp32 arithmetic (u = 2^-24):
+  logp:    1e-5 for the exponentials and the merging of partial sums, n u for the n terms that a thread adds one
+           after another in the careful form (V / 32 where a warp has the row, V / 128 where a block has it), and
+           4 u (|logp| + |scale (l_y - r)|) for the subtraction, the product with the scale and the roundings.
+  dlogits = g (1[v = y] - p): p is off by the same (1e-5 + n u) of itself and by 3 u |t| for its exponent (|t| < 200
+           where p counts: 4e-5); g by 8 u (seven products and an exponential of one unit in the last place) and by
+           what the derivative of the loss makes of the error of logp; then half a step of the output type, and what
+           flushes to zero (2^-126 of g).
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from bit_nf4_quantized_quant_b200 import _ops as ops
+from oracle import training as tr
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+HALF = {"bf16": 2.0 ** -8, "fp32": U}
+# a warp a row, a block a row, clusters of CTAs, rows beyond the registers of a block
+SHAPES = [(9, 300), (700, 5003), (9, 40000), (330, 20001), (3, 131072)]
+
+
+def _rows_at(M, V, dtype, at):
+    """Rows of equal logits near `at` (even ones) and of logits up to three steps of the type towards 0 from there
+    (odd ones), with a target each."""
+    g = np.random.default_rng(V)
+    l = torch.full((M, V), at, dtype=torch.float64)
+    step = 2.0 ** (math.floor(math.log2(abs(at))) - (7 if dtype == "bf16" else 23))
+    l[1::2] -= torch.from_numpy(g.integers(0, 4, l[1::2].shape)) * math.copysign(step, at)
+    return l.to(DT[dtype]).cuda(), g.integers(0, V, M)
+
+
+def _check_rows(l, yn, tau, dtype):
+    """Log-probabilities of the three entry points and gradients of both losses (a policy loss of ratio 1 and
+    advantage -1: g = 1; an IPO loss of one row against none a pair: g = 2 (logp - 1))."""
+    M, V = l.shape
+    y = torch.from_numpy(yn).cuda()
+    l64 = l.double().cpu().numpy()
+    ref, ls, _ = tr.token_logprob(l64, yn, tau)
+    n = V / (32 if V * l.element_size() <= 8192 + 16 else 128)
+    e_lp = 1e-5 + n * U + 4 * U * (np.abs(ref) + np.abs(tau * (l64[np.arange(M), yn] - l64.max(-1))))
+    ones = torch.ones(M, device="cuda")
+    pol = ops.policy_loss(l, y, -ones, ones, None, None, logit_scale=tau)
+    cu = torch.arange(M + 1, device="cuda", dtype=torch.int32).repeat_interleave(2)[1:].contiguous()
+    pre = ops.preference_loss(l, y, cu, None, 0.5, kind=ops.QLORA_PREF_IPO, grad_scale=M, logit_scale=tau)
+    for name, lp in (("token", ops.token_logprob(l, y, tau)), ("policy", pol.logp), ("preference", pre.logp)):
+        err = np.abs(lp.double().cpu().numpy() - ref)
+        assert (err <= e_lp).all(), (name, err.max())
+    p = np.exp(ls)
+    want = np.where(np.arange(V)[None] == yn[:, None], 1.0, 0.0) - p
+    e_lp = e_lp[:, None]
+    for name, got, g, e_g in (("policy", pol.dlogits, np.ones((M, 1)), 0.0),
+                              ("preference", pre.dlogits, 2 * (ref - 1.0)[:, None], 2 * e_lp)):
+        got, g = got.double().cpu().numpy(), g * tau
+        e = (e_g * tau + 8 * U * np.abs(g)) * np.where(want != 0, 1.0, 0.0)
+        lim = np.abs(g) * p * (e_lp + 5e-5) + e + HALF[dtype] * np.abs(want * g) + (np.abs(g) + tau) * 2.0 ** -126
+        bad = ~(np.abs(got - want * g) <= lim * 1.0001)
+        assert not bad.any(), (name, bad.sum(), np.abs(got - want * g)[bad].max(), np.argwhere(bad)[:3])
+
+
+# (about) the logits, the scale: |scale * logits| from 1e6 on, up to 2^45
+FAR = [(1e6, 1.0), (-1e7, 1.0), (2e7, 1.25), (-2e7, 1.0), (1e8, 1.0), (-1e8, 1.25), (1e9, 1.0), (-1e9, 1.0),
+       (-1e9, 1e-3), (3e3, 1e4), (30.0, 2.0 ** 40)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,V", SHAPES)
+@pytest.mark.parametrize("at,tau", FAR)
+def test_rows_far_from_zero(at, tau, M, V, dtype):
+    """What the log-probability keeps of logits that are large and alike: their differences, whole."""
+    _check_rows(*_rows_at(M, V, dtype, at), tau, dtype)
