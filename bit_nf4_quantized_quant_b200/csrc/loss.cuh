@@ -367,11 +367,21 @@ __device__ __forceinline__ KS sum_pass(const uint4 (&v)[NV], float x1, float c, 
     return acc;
 }
 
-// An element's exponent in the gradient; c_lo would be lost in a bf16 result.
+// An element's exponent in the gradient.  In bf16 c_lo l is left out an element, and put into the
+// factor before the exponential once a row for l = k / c, about the row's largest logit
+// (grad_factor): what remains is c_lo (l - k / c), below 2^-23 of the exponent c l - k, which is
+// lost in a bf16 result.
 template <typename T>
 __device__ __forceinline__ float grad_exp(float l, float c, float c_lo, float k) {
     const float t = fmaf(l, c, -k);
     return sizeof(T) == 4 ? fmaf(l, c_lo, t) : t;
+}
+
+// q of -g p = q ex2(grad_exp), from the row's sum s; c_rel = c_lo / c.
+template <typename T>
+__device__ __forceinline__ float grad_factor(float g, KS t, float c_rel) {
+    const float q = -g / t.s;
+    return sizeof(T) == 4 ? q : q * ex2(t.k * c_rel);
 }
 
 // -g p = q ex2(c l - k); the target's element is at_y, which the thread that has just written there writes:
@@ -446,8 +456,8 @@ __device__ __forceinline__ void zero_row(T* o, int V, int v0, int v1, uint32_t r
 }
 
 // The gradient of a row element by element: in the careful form, and for a
-// gradient row whose 16-byte boundaries are not the logits' (q = -g / S, and
-// k as in the vector path, whose results these equal bit for bit).
+// gradient row whose 16-byte boundaries are not the logits' (q and k as in the
+// vector path, whose results these equal bit for bit).
 template <typename T>
 __device__ __noinline__ void scalar_grad(const T* x, T* o, int V, int y, int v0, int v1, float c, float c_lo, bool careful,
                                          MS ms, float k, float q, float g, float at_y, uint32_t rank) {
@@ -719,7 +729,7 @@ struct GradArgs {
     const void* logits;
     int64_t M, ld;
     int V;
-    float tau, c, c_lo;
+    float tau, c, c_lo, c_rel;   // c_rel = c_lo / c
     const int64_t* targets;
     const double* lpd;           // [M] of k_token_logprob
     const float2* stats;         // [M] of k_token_logprob
@@ -758,7 +768,7 @@ __device__ __forceinline__ void grad_chunk(const GradArgs& a, int64_t row, int c
             v[u] = i0 + u * NT < sp.nv ? ld_v4(xv + i0 + u * NT) : make_uint4(0, 0, 0, 0);
     }
     const float g = y >= 0 ? coef() * a.tau : 0.f;
-    const float q = -g / (careful ? -st.y : st.y);
+    const float q = careful ? g / st.y : grad_factor<T>(g, KS{st.x, st.y}, a.c_rel);
     auto one = [&](float l) { return q * ex2(careful ? (l - st.x) * a.c : grad_exp<T>(l, a.c, a.c_lo, st.x)); };
     auto at_y = [&] { return -g * expm1f((float)a.lpd[row]); };
     auto put = [&](int e) {
@@ -1092,7 +1102,7 @@ struct PolicyArgs {
     const void* logits;
     int64_t M, ld;
     int V;
-    float tau, c, c_lo;          // c + c_lo = tau log2 e
+    float tau, c, c_lo, c_rel;   // c + c_lo = tau log2 e, c_rel = c_lo / c
     const int64_t* targets;
     const float* old_logp;       // [M], or null: the ratio is 1 (its gradient stays)
     const float* ref_logp;       // [M], or null: no KL term
@@ -1227,7 +1237,7 @@ __global__ void __launch_bounds__(kBlockThreads) k_policy_block(const PolicyArgs
         const float g = fine ? policy_row(a, row, lp, A, w, old, ref, rank == 0 && tid == 0) : 0.f;
         const float at_y = g * lp2_rest(lp);
         if (tid == 0) {
-            sh.row = make_float4(t.k, -g / t.s, g, fine ? 0.f : 1.f);
+            sh.row = make_float4(t.k, grad_factor<T>(g, t, a.c_rel), g, fine ? 0.f : 1.f);
             sh.at_y = at_y;
         }
     }
@@ -1291,7 +1301,7 @@ __global__ void __launch_bounds__(kBlockThreads) k_policy_short(const PolicyArgs
     const float g = policy_row(a, (int)row, lp, A, w, old, ref, id == 0);
     if (a.out == nullptr) return;
     const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
-    const float k = t.k, q = -g / (careful ? ms.s : t.s);
+    const float k = t.k, q = careful ? -g / ms.s : grad_factor<T>(g, t, a.c_rel);
     if (g == 0.f) {
         zero_short_row<T, NT>(o, V);
     } else if (careful || !same) {

@@ -1083,13 +1083,14 @@ bool rows_collide(const void* logits, int64_t ld, const void* grad, int64_t ldd,
     return at < (uint64_t)V * es || (uint64_t)(ld - V) * es < at;
 }
 
-// The fp32 number c below tau log2 e, and the rest of it.  The rest is positive:
-// with another sign, or 0, the kernels' -inf c + -inf c_lo would be a NaN.
-void split_c(float tau, float* c, float* c_lo) {
+// The fp32 number c below tau log2 e, and the rest of it, also over c.  The rest is
+// positive: with another sign, or 0, the kernels' -inf c + -inf c_lo would be a NaN.
+void split_c(float tau, float* c, float* c_lo, float* c_rel = nullptr) {
     const double full = (double)tau * 1.4426950408889634074;
     *c = (float)full;
     if ((double)*c >= full) *c = std::nextafterf(*c, 0.f);
     *c_lo = (float)(full - (double)*c);
+    if (c_rel) *c_rel = (float)((full - (double)*c) / (double)*c);
 }
 
 template <typename KArg>
@@ -1719,7 +1720,7 @@ int preference_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t
     a.grad_scale = grad_scale; a.loss = loss; a.rewards = rewards; a.dlogp = dlogits ? dlogp : nullptr;
     loss::GradArgs g{};
     g.logits = logits; g.M = M; g.V = (int)V; g.ld = ld; g.tau = logit_scale;
-    split_c(logit_scale, &g.c, &g.c_lo);
+    split_c(logit_scale, &g.c, &g.c_lo, &g.c_rel);
     g.targets = targets; g.lpd = lpd; g.stats = stats; g.dlogp = dlogp; g.out = dlogits; g.ldo = ldd; g.chunks = (int)chunks;
     if (dlogits && M <= loss::kFewRows && P <= loss::kFewPairs) {
         const loss::FewArgs fa{a, g};
@@ -1769,7 +1770,7 @@ int policy_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld,
     cudaStream_t st = (cudaStream_t)stream;
     loss::PolicyArgs a{};
     a.logits = logits; a.M = M; a.V = (int)V; a.ld = ld; a.tau = logit_scale;
-    split_c(logit_scale, &a.c, &a.c_lo);
+    split_c(logit_scale, &a.c, &a.c_lo, &a.c_rel);
     a.targets = targets; a.old_logp = old_logp; a.ref_logp = ref_logp; a.adv = advantages; a.weight = weights;
     a.lo = 1.f - clip_low; a.hi = 1.f + clip_high; a.kl = kl_coef; a.grad_scale = grad_scale;
     a.logp = logp; a.part = static_cast<float4*>(ws); a.out = dlogits; a.ldo = ldd;

@@ -75,3 +75,29 @@ FAR = [(1e6, 1.0), (-1e7, 1.0), (2e7, 1.25), (-2e7, 1.0), (1e8, 1.0), (-1e8, 1.2
 def test_rows_far_from_zero(at, tau, M, V, dtype):
     """What the log-probability keeps of logits that are large and alike: their differences, whole."""
     _check_rows(*_rows_at(M, V, dtype, at), tau, dtype)
+
+
+# offsets at which the rest of the scale times log2 e, 2^-24 to 2^-23 of it, times the logits is more than bf16 keeps
+NEAR = [(1e4, 1.25), (-1e5, 1.25), (1e5, 1.0), (-1e5, 0.6), (3e5, 1.0), (-5e5, 1.25), (1e6, 0.6), (-1e6, 0.6)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,V", SHAPES)
+@pytest.mark.parametrize("at,tau", NEAR)
+def test_rows_with_a_large_offset(at, tau, M, V, dtype):
+    _check_rows(*_rows_at(M, V, dtype, at), tau, dtype)
+
+
+def test_gradient_rows_with_a_large_offset_at_another_alignment():
+    """A gradient row whose 16-byte boundaries are not the logits' equals the one whose boundaries are."""
+    for M, V in ((9, 300), (9, 40001)):
+        l, yn = _rows_at(M, V, "bf16", -1e5)
+        y, w = torch.from_numpy(yn).cuda(), torch.ones(M, device="cuda")
+        cu = torch.tensor([0, 4, M], dtype=torch.int32, device="cuda")
+        out = torch.empty((M * (V + 7) + 1,), dtype=torch.bfloat16, device="cuda")
+        dl = out.as_strided((M, V), (V + 7, 1), 1)
+        for f in (lambda **k: ops.policy_loss(l, y, -w, w, None, None, logit_scale=1.25, **k),
+                  lambda **k: ops.preference_loss(l, y, cu, None, 0.1, logit_scale=1.25, **k)):
+            want = f().dlogits
+            f(dlogits=dl)
+            assert torch.equal(dl, want)
