@@ -1154,7 +1154,9 @@ __device__ __forceinline__ float lp2_minus(Lp2 lp, float x) {
 __device__ __forceinline__ float lp2_rest(Lp2 lp) { return -expm1f((lp.hi + lp.lo) * kLn2); }
 
 // The row's loss terms (written by the thread that is told to) and d loss /
-// d logit scale: what multiplies 1[v = y] - p_v.
+// d logit scale: what multiplies 1[v = y] - p_v.  Without a coefficient the KL
+// term is left out rather than multiplied by 0: it is infinite in fp32 from a
+// distance of 88.7 on.
 __device__ __forceinline__ float policy_row(const PolicyArgs& a, int row, Lp2 lp, float A, float w, float old,
                                             float ref, bool put) {
     const float rho = a.old_logp ? exp2f(lp2_minus(lp, old)) : 1.f;
@@ -1165,9 +1167,10 @@ __device__ __forceinline__ float policy_row(const PolicyArgs& a, int row, Lp2 lp
         const float pol = -(clipped ? held : free_), kl = em - d;
         const float r = lp.hi * kLn2;
         a.logp[row] = fabsf(r) < INFINITY ? r + (fmaf(lp.hi, kLn2, -r) + fmaf(lp.hi, kLn2Lo, lp.lo * kLn2)) : r;
-        a.part[row] = make_float4(w * (pol + a.kl * kl), w * pol, w * kl, clipped ? w : 0.f);
+        a.part[row] = make_float4(w * (a.kl != 0.f ? pol + a.kl * kl : pol), w * pol, w * kl, clipped ? w : 0.f);
     }
-    return w * ((clipped ? 0.f : -free_) - a.kl * em) * a.grad_scale * a.tau;
+    const float dp = clipped ? 0.f : -free_;
+    return w * (a.kl != 0.f ? dp - a.kl * em : dp) * a.grad_scale * a.tau;
 }
 
 // A row's gradient depends on that row alone, so each row is read once, held

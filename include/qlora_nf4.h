@@ -385,7 +385,8 @@ QLORA_API int preference_loss(const void* logits, int dtype, int64_t M, int64_t 
  *   rho  = exp(logp - old_logp)    (old_logp NULL: 1, with the same gradient)
  *   pol  = -min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A)
  *   kl   = exp(d) - d - 1, d = ref_logp - logp    (ref_logp NULL: 0)
- *   loss = sum of weights (pol + kl_coef kl)
+ *   loss = sum of weights (pol + kl_coef kl); with kl_coef = 0 kl is summed for
+ *          stats alone
  *   stats [4] = loss, sum w pol, sum w kl, sum of w over the clipped rows
  * The gradient of pol is zero where the clipped term is the strictly smaller
  * one and -rho A elsewhere.  The weights carry the mask and the normalisation

@@ -101,3 +101,19 @@ def test_gradient_rows_with_a_large_offset_at_another_alignment():
             want = f().dlogits
             f(dlogits=dl)
             assert torch.equal(dl, want)
+
+
+@pytest.mark.parametrize("V", [200, 9000, 70000])
+def test_policy_reference_without_a_coefficient(V):
+    """kl_coef = 0 with a reference whose distance is beyond the exponential's range: the loss and the gradient are
+    those without a reference, and the KL sum alone is infinite."""
+    M = 8
+    l = torch.randn((M, V), device="cuda")
+    y = torch.arange(M, device="cuda")
+    w = torch.ones(M, device="cuda")
+    old = ops.token_logprob(l, y) - 0.1
+    for far in (old + 100, old + 1000, old.new_full((M,), 1e30)):
+        a = ops.policy_loss(l, y, w, w, old, None)
+        b = ops.policy_loss(l, y, w, w, old, far, kl_coef=0.0)
+        assert torch.isfinite(a.dlogits).all() and torch.equal(a.dlogits, b.dlogits) and torch.equal(a.logp, b.logp)
+        assert torch.equal(a.stats[[0, 1, 3]], b.stats[[0, 1, 3]]) and b.stats[2] == float("inf")
