@@ -1156,11 +1156,11 @@ __device__ __forceinline__ float lp2_rest(Lp2 lp) { return -expm1f((lp.hi + lp.l
 // The row's loss terms (written by the thread that is told to) and d loss /
 // d logit scale: what multiplies 1[v = y] - p_v.  Without a coefficient the KL
 // term is left out rather than multiplied by 0: it is infinite in fp32 from a
-// distance of 88.7 on.
+// distance of 88.7 on.  So is the ratio, which an advantage of 0 makes 0.
 __device__ __forceinline__ float policy_row(const PolicyArgs& a, int row, Lp2 lp, float A, float w, float old,
                                             float ref, bool put) {
     const float rho = a.old_logp ? exp2f(lp2_minus(lp, old)) : 1.f;
-    const float free_ = rho * A, held = fminf(fmaxf(rho, a.lo), a.hi) * A;
+    const float free_ = A == 0.f && rho == INFINITY ? 0.f : rho * A, held = fminf(fmaxf(rho, a.lo), a.hi) * A;
     const bool clipped = held < free_;
     const float d = a.ref_logp ? -lp2_minus(lp, ref) * kLn2 : 0.f, em = expm1f(d);
     if (put) {

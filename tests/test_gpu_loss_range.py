@@ -117,3 +117,23 @@ def test_policy_reference_without_a_coefficient(V):
         b = ops.policy_loss(l, y, w, w, old, far, kl_coef=0.0)
         assert torch.isfinite(a.dlogits).all() and torch.equal(a.dlogits, b.dlogits) and torch.equal(a.logp, b.logp)
         assert torch.equal(a.stats[[0, 1, 3]], b.stats[[0, 1, 3]]) and b.stats[2] == float("inf")
+
+
+@pytest.mark.parametrize("V", [200, 9000, 70000])
+def test_policy_ratio_beyond_the_range(V):
+    """A ratio above the largest fp32 number: nothing at advantage 0, the clipped term where it is the smaller one,
+    infinite where it is not; and a NaN among the logits stays one at advantage 0."""
+    M = 8
+    l = torch.randn((M, V), device="cuda")
+    y = torch.arange(M, device="cuda")
+    w = torch.ones(M, device="cuda")
+    old = ops.token_logprob(l, y) - 100
+    o = ops.policy_loss(l, y, 0 * w, w, old, None)
+    assert (o.stats == 0).all() and (o.dlogits == 0).all()
+    o = ops.policy_loss(l, y, w, w, old, None, clip_high=0.25)
+    assert o.stats.tolist() == [-10.0, -10.0, 0.0, 8.0] and (o.dlogits == 0).all()
+    o = ops.policy_loss(l, y, -w, w, old, None)
+    assert (o.stats[:2] == float("inf")).all() and o.stats[3] == 0
+    l[3, V - 1] = float("nan")
+    o = ops.policy_loss(l, y, 0 * w, w, old, None)
+    assert torch.isnan(o.stats[:2]).all() and torch.isnan(o.dlogits[3]).all() and (o.dlogits[[0, 1, 2, 4, 5, 6, 7]] == 0).all()
