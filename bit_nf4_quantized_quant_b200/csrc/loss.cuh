@@ -918,7 +918,7 @@ struct PairTerms {
             g = beta * (eps * (1. - sg) - (1. - eps) * sg);
         } else if (a.kind == QLORA_PREF_HINGE) {
             loss = zz < 1. ? 1. - zz : zz == zz ? 0. : zz;
-            g = zz < 1. ? -beta : 0.;
+            g = zz < 1. ? -beta : zz == zz ? 0. : zz;        // NaN stays visible
         } else {
             const double q = delta - 0.5 / beta;
             loss = q * q;

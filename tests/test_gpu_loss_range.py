@@ -137,3 +137,18 @@ def test_policy_ratio_beyond_the_range(V):
     l[3, V - 1] = float("nan")
     o = ops.policy_loss(l, y, 0 * w, w, old, None)
     assert torch.isnan(o.stats[:2]).all() and torch.isnan(o.dlogits[3]).all() and (o.dlogits[[0, 1, 2, 4, 5, 6, 7]] == 0).all()
+
+
+@pytest.mark.parametrize("M,P", [(8, 2), (600, 3)])
+@pytest.mark.parametrize("kind", [ops.QLORA_PREF_SIGMOID, ops.QLORA_PREF_HINGE, ops.QLORA_PREF_IPO])
+def test_a_nan_shows_in_its_pair_alone(kind, M, P):
+    """A NaN logit in a row that counts: its pair's gradient and rewards and the loss are NaN, the other pairs' not."""
+    l = torch.randn((M, 200), device="cuda")
+    l[0, 3] = float("nan")
+    y = torch.arange(M, device="cuda") % 200
+    cu = torch.linspace(0, M, 2 * P + 1, device="cuda").int()
+    o = ops.preference_loss(l, y, cu, None, 0.1, kind=kind)
+    a, b = int(cu[1]), int(cu[2])
+    assert torch.isnan(o.loss) and torch.isnan(o.rewards[0]) and torch.isfinite(o.rewards[1:]).all()
+    assert torch.isnan(o.dlogits[:b]).all() and torch.isfinite(o.dlogits[b:]).all()
+    assert torch.isnan(o.logp[0]) and torch.isfinite(o.logp[1:]).all() and a < b
