@@ -913,7 +913,8 @@ struct PairTerms {
         double g;                                // d loss / d delta
         if (a.kind == QLORA_PREF_SIGMOID) {
             const double e = exp(-fabs(zz)), sp = log1p(e);
-            loss = (1. - eps) * (sp + fmax(-zz, 0.)) + (eps != 0. ? eps * (sp + fmax(zz, 0.)) : 0.);
+            // a side without weight may be infinite (a target of probability 0)
+            loss = (eps != 1. ? (1. - eps) * (sp + fmax(-zz, 0.)) : 0.) + (eps != 0. ? eps * (sp + fmax(zz, 0.)) : 0.);
             const double sg = zz >= 0. ? e / (1. + e) : 1. / (1. + e);      // sigmoid(-z)
             g = beta * (eps * (1. - sg) - (1. - eps) * sg);
         } else if (a.kind == QLORA_PREF_HINGE) {

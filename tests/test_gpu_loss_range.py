@@ -152,3 +152,20 @@ def test_a_nan_shows_in_its_pair_alone(kind, M, P):
     assert torch.isnan(o.loss) and torch.isnan(o.rewards[0]) and torch.isfinite(o.rewards[1:]).all()
     assert torch.isnan(o.dlogits[:b]).all() and torch.isfinite(o.dlogits[b:]).all()
     assert torch.isnan(o.logp[0]) and torch.isfinite(o.logp[1:]).all() and a < b
+
+
+@pytest.mark.parametrize("M", [4, 600])
+@pytest.mark.parametrize("eps", [0.0, 1.0])
+def test_preference_target_of_probability_zero(eps, M):
+    """A target at -inf makes its sequence's reward -inf.  The side of the smoothed loss that has no weight may then be
+    infinite without a trace: with all weight on the other label the loss is that of -z."""
+    l = torch.randn((M, 200), device="cuda")
+    y = torch.arange(M, device="cuda") % 200
+    cu = torch.tensor([0, 1, 2, 3, 4], dtype=torch.int32, device="cuda")
+    worse = 0 if eps else 1                                    # the sequence whose loss of probability is no loss
+    base = ops.preference_loss(l[2:4], y[2:4], cu[:3], None, 0.1, label_smoothing=eps)
+    l[worse, worse] = -float("inf")
+    o = ops.preference_loss(l, y, cu, None, 0.1, label_smoothing=eps)
+    assert o.rewards[worse] == -float("inf") and torch.isfinite(o.rewards[1 - worse])
+    assert abs(2 * o.loss.item() - base.loss.item()) <= 1e-6
+    assert (o.dlogits[:2] == 0).all() and torch.isfinite(o.dlogits).all()
