@@ -391,16 +391,24 @@ def _step():
     return _step_mod
 
 
-def _raw(stream):
-    return None if stream is None else stream.cuda_stream
+def _run(stream, fn, *args, ws=None):
+    """fn(*args, stream handle); the outputs.
 
-
-def _keep(stream, *tensors):
-    """Memory taken from the current stream's pool and used on `stream` goes back to it only after that use."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    On a stream that is not the current one, what fn allocates comes from that stream's pool: a block that was freed
+    on the current stream may still be in use by work queued there.  Outputs go back to a pool only when the work
+    queued by then on both streams is done (the current one is where the caller reads them)."""
+    if stream is None:
+        return fn(*args, None)
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        out = fn(*args, stream.cuda_stream)
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(stream)
+            t.record_stream(here)
+    if ws is not None:
+        ws.record_stream(stream)
+    return out
 
 
 @dataclass
@@ -435,21 +443,18 @@ def act8_quantize(X: torch.Tensor, fmt: int = QLORA_ACT8_INT8, out: Act8Tensor |
                   stream=None) -> Act8Tensor:
     """bf16 X [M, K] (device) -> 8-bit checkpoint."""
     if out is None:
-        codes, scales = _step().act8_quantize(X, fmt, None, None, _raw(stream))
-        _keep(stream, codes, scales)
+        codes, scales = _run(stream, _step().act8_quantize, X, fmt, None, None)
         return Act8Tensor(codes, scales, *X.shape, int(fmt))
     if (out.M, out.K) != X.shape:
         raise ValueError(f"out: a checkpoint of {tuple(X.shape)} wanted, got {(out.M, out.K)}")
-    _step().act8_quantize(X, fmt, out.codes, out.scales, _raw(stream))
+    _run(stream, _step().act8_quantize, X, fmt, out.codes, out.scales)
     out.fmt = int(fmt)
     return out
 
 
 def act8_dequant(x: Act8Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """8-bit checkpoint -> the bf16 tensor it stands for."""
-    out = _step().act8_dequant(x.codes, x.scales, x.M, x.K, x.fmt, out, _raw(stream))
-    _keep(stream, out)
-    return out
+    return _run(stream, _step().act8_dequant, x.codes, x.scales, x.M, x.K, x.fmt, out)
 
 
 def qlora_act8_workspace_bytes(M: int, N: int, K: int, r: int, dropout: bool = False) -> int:
@@ -466,13 +471,8 @@ def act8_workspace(M: int, N: int, K: int, r: int, dropout: bool = False, device
 def qlora_linear_bwd_act8(X: Act8Tensor, dY, w: NF4Weight, A, B, scaling: float, T=None, dX=None, dA=None, dB=None,
                           dropout_p: float = 0.0, seed: int = 0, offset: int = 0, ws=None, stream=None):
     """qlora_linear_bwd (dropout_p > 0: qlora_linear_bwd_dropout) from an 8-bit checkpoint of X; (dX, dA, dB)."""
-    if stream is not None and ws is None:
-        ws = act8_workspace(X.M, w.N, w.K, A.shape[0], dropout_p > 0, X.codes.device)
-    out = _step().qlora_linear_bwd_act8(X.codes, X.scales, X.M, X.K, X.fmt, w.packed, w.codes, w.scale, w.mean, w.N,
-                                        w.K, w.quant_type, dY, A, B, scaling, dropout_p, seed, offset, T, dX, dA, dB,
-                                        ws, _raw(stream))
-    _keep(stream, *out, ws)
-    return out
+    return _run(stream, _step().qlora_linear_bwd_act8, X.codes, X.scales, X.M, X.K, X.fmt, w.packed, w.codes, w.scale,
+                w.mean, w.N, w.K, w.quant_type, dY, A, B, scaling, dropout_p, seed, offset, T, dX, dA, dB, ws, ws=ws)
 
 
 # --------------------------------------------------------------------------
@@ -492,9 +492,7 @@ def loss_workspace(M: int, device="cuda") -> torch.Tensor:
 def token_logprob(logits: torch.Tensor, targets: torch.Tensor, logit_scale: float = 1.0, out=None,
                   stream=None) -> torch.Tensor:
     """fp32 [M]: log-probability of each row's target (0 where the target is outside [0, V))."""
-    out = _step().token_logprob(logits, targets, logit_scale, out, _raw(stream))
-    _keep(stream, out)
-    return out
+    return _run(stream, _step().token_logprob, logits, targets, logit_scale, out)
 
 
 @dataclass
@@ -513,12 +511,9 @@ def preference_loss(logits, targets, cu_seqlens, ref_logp, beta: float, kind: in
 
     cu_seqlens int32 [2 P + 1]: pair p prefers sequence 2p to sequence 2p + 1.  ref_logp fp32 [M] or None.
     dlogits may be the logits themselves; with want_grad=False and no dlogits, the loss alone."""
-    if stream is not None and ws is None:
-        ws = loss_workspace(logits.shape[0], logits.device)
-    out = _step().preference_loss(logits, targets, cu_seqlens, ref_logp, beta, kind, label_smoothing, margin, average,
-                                  logit_scale, grad_scale, dlogits, want_grad, ws, _raw(stream))
-    _keep(stream, *out, ws)
-    return PreferenceOut(*out)
+    return PreferenceOut(*_run(stream, _step().preference_loss, logits, targets, cu_seqlens, ref_logp, beta, kind,
+                               label_smoothing, margin, average, logit_scale, grad_scale, dlogits, want_grad, ws,
+                               ws=ws))
 
 
 @dataclass
@@ -535,12 +530,8 @@ def policy_loss(logits, targets, advantages, weights, old_logp, ref_logp, clip_l
 
     advantages, weights fp32 [M]; old_logp, ref_logp fp32 [M] or None (ratio 1, no KL term).
     dlogits may be the logits themselves; with want_grad=False and no dlogits, the loss alone."""
-    if stream is not None and ws is None:
-        ws = loss_workspace(logits.shape[0], logits.device)
-    out = _step().policy_loss(logits, targets, advantages, weights, old_logp, ref_logp, clip_low, clip_high, kl_coef,
-                              logit_scale, grad_scale, dlogits, want_grad, ws, _raw(stream))
-    _keep(stream, *out, ws)
-    return PolicyOut(*out)
+    return PolicyOut(*_run(stream, _step().policy_loss, logits, targets, advantages, weights, old_logp, ref_logp,
+                           clip_low, clip_high, kl_coef, logit_scale, grad_scale, dlogits, want_grad, ws, ws=ws))
 
 
 def qlora_device_status(reset: bool = True) -> int:
