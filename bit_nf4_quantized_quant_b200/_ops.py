@@ -131,6 +131,24 @@ def _stream(stream=None):
     return stream.cuda_stream
 
 
+def _on(stream, make):
+    """make(), whose memory comes from the pool of the stream that the call runs on: a block that was freed on the
+    current stream may still be in use by work queued there.  The current stream, where the caller reads the result,
+    holds it as well."""
+    if stream is None:
+        return make()
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        out = make()
+    for t in (out,) if isinstance(out, torch.Tensor) else (out.packed, out.codes, out.scale, out.mean):
+        t.record_stream(here)
+    return out
+
+
+def _empty(shape: tuple, device, stream) -> torch.Tensor:
+    return _on(stream, lambda: torch.empty(shape, dtype=torch.bfloat16, device=device))
+
+
 def _bits(t: torch.Tensor) -> torch.Tensor:
     assert t.dtype == torch.bfloat16, t.dtype
     assert t.is_contiguous()
@@ -185,7 +203,7 @@ def nf4_quantize_dq(W: torch.Tensor, out: NF4Weight | None = None, stream=None) 
     W = _bits(W)
     N, K = W.shape
     if out is None:
-        out = NF4Weight.empty(N, K, W.device)
+        out = _on(stream, lambda: NF4Weight.empty(N, K, W.device))
     _check("nf4_quantize_dq", lib().nf4_quantize_dq(_ptr(W), N, K, _ptr(out.packed), _ptr(out.codes),
                                                     _ptr(out.scale), _ptr(out.mean), _stream(stream)))
     return out
@@ -196,7 +214,7 @@ def quant4_quantize_dq(W: torch.Tensor, quant_type: int, out: NF4Weight | None =
     W = _bits(W)
     N, K = W.shape
     if out is None:
-        out = NF4Weight.empty(N, K, W.device, quant_type)
+        out = _on(stream, lambda: NF4Weight.empty(N, K, W.device, quant_type))
     out.quant_type = int(quant_type)
     _check("quant4_quantize_dq", lib().quant4_quantize_dq(_ptr(W), N, K, int(quant_type), _ptr(out.packed),
                                                           _ptr(out.codes), _ptr(out.scale), _ptr(out.mean),
@@ -208,7 +226,7 @@ def nf4_dequant_merge(w: NF4Weight, A, B, scaling: float, out: torch.Tensor | No
                       stream=None) -> torch.Tensor:
     """Dense bf16 W' + scaling * B A (the merged weight of the adapted layer)."""
     if out is None:
-        out = torch.empty((w.N, w.K), dtype=torch.bfloat16, device=w.packed.device)
+        out = _empty((w.N, w.K), w.packed.device, stream)
     st = w.c_struct()
     _check("nf4_dequant_merge", lib().nf4_dequant_merge(ctypes.byref(st), _ptr(_bits(A)), _ptr(_bits(B)),
                                                         A.shape[0], float(scaling), _ptr(out), _stream(stream)))
@@ -248,7 +266,7 @@ def adamw_8bit_step(p: torch.Tensor, g: torch.Tensor, state: AdamW8State, step: 
 
 def nf4_dequant(w: NF4Weight, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     if out is None:
-        out = torch.empty((w.N, w.K), dtype=torch.bfloat16, device=w.packed.device)
+        out = _empty((w.N, w.K), w.packed.device, stream)
     st = w.c_struct()
     _check("nf4_dequant", lib().nf4_dequant(ctypes.byref(st), _ptr(out), _stream(stream)))
     return out
@@ -269,9 +287,9 @@ def qlora_linear_fwd(X, w: NF4Weight, A, B, scaling: float, Y=None, T_out=None, 
     """Y = X W'^T + s (X A^T) B^T; returns Y (and fills T_out when given)."""
     M = X.shape[0]
     if Y is None:
-        Y = torch.empty((M, w.N), dtype=torch.bfloat16, device=X.device)
+        Y = _empty((M, w.N), X.device, stream)
     if ws is None:
-        ws = workspace(M, w.N, w.K, A.shape[0], X.device)
+        ws = _on(stream, lambda: workspace(M, w.N, w.K, A.shape[0], X.device))
     st = w.c_struct()
     _check("qlora_linear_fwd", lib().qlora_linear_fwd(
         _ptr(_bits(X)), M, ctypes.byref(st), _ptr(_bits(A)), _ptr(_bits(B)), A.shape[0], float(scaling),
@@ -286,13 +304,13 @@ def qlora_linear_bwd(X, dY, w: NF4Weight, A, B, scaling: float, T=None, dX=None,
     r = A.shape[0]
     dev = X.device
     if dX is None:
-        dX = torch.empty((M, w.K), dtype=torch.bfloat16, device=dev)
+        dX = _empty((M, w.K), dev, stream)
     if dA is None:
-        dA = torch.empty((r, w.K), dtype=torch.bfloat16, device=dev)
+        dA = _empty((r, w.K), dev, stream)
     if dB is None:
-        dB = torch.empty((w.N, r), dtype=torch.bfloat16, device=dev)
+        dB = _empty((w.N, r), dev, stream)
     if ws is None:
-        ws = workspace(M, w.N, w.K, r, dev)
+        ws = _on(stream, lambda: workspace(M, w.N, w.K, r, dev))
     st = w.c_struct()
     _check("qlora_linear_bwd", lib().qlora_linear_bwd(
         _ptr(_bits(X)), _ptr(_bits(dY)), M, ctypes.byref(st), _ptr(_bits(A)), _ptr(_bits(B)), r, float(scaling),
@@ -316,9 +334,9 @@ def qlora_linear_fwd_dropout(X, w: NF4Weight, A, B, scaling: float, dropout_p: f
     """qlora_linear_fwd with LoRA dropout on the branch input (mask from (seed, offset))."""
     M = X.shape[0]
     if Y is None:
-        Y = torch.empty((M, w.N), dtype=torch.bfloat16, device=X.device)
+        Y = _empty((M, w.N), X.device, stream)
     if ws is None:
-        ws = dropout_workspace(M, w.N, w.K, A.shape[0], X.device)
+        ws = _on(stream, lambda: dropout_workspace(M, w.N, w.K, A.shape[0], X.device))
     st = w.c_struct()
     _check("qlora_linear_fwd_dropout", lib().qlora_linear_fwd_dropout(
         _ptr(_bits(X)), M, ctypes.byref(st), _ptr(_bits(A)), _ptr(_bits(B)), A.shape[0], float(scaling),
@@ -333,13 +351,13 @@ def qlora_linear_bwd_dropout(X, dY, w: NF4Weight, A, B, scaling: float, dropout_
     r = A.shape[0]
     dev = X.device
     if dX is None:
-        dX = torch.empty((M, w.K), dtype=torch.bfloat16, device=dev)
+        dX = _empty((M, w.K), dev, stream)
     if dA is None:
-        dA = torch.empty((r, w.K), dtype=torch.bfloat16, device=dev)
+        dA = _empty((r, w.K), dev, stream)
     if dB is None:
-        dB = torch.empty((w.N, r), dtype=torch.bfloat16, device=dev)
+        dB = _empty((w.N, r), dev, stream)
     if ws is None:
-        ws = dropout_workspace(M, w.N, w.K, r, dev)
+        ws = _on(stream, lambda: dropout_workspace(M, w.N, w.K, r, dev))
     st = w.c_struct()
     _check("qlora_linear_bwd_dropout", lib().qlora_linear_bwd_dropout(
         _ptr(_bits(X)), _ptr(_bits(dY)), M, ctypes.byref(st), _ptr(_bits(A)), _ptr(_bits(B)), r, float(scaling),
@@ -557,7 +575,7 @@ def qlora_linear_fwd_noalloc(X, w: NF4Weight, A, B, scaling: float, Y=None, T_ou
     """qlora_linear_fwd on the library's fixed static scratch (no workspace argument)."""
     M = X.shape[0]
     if Y is None:
-        Y = torch.empty((M, w.N), dtype=torch.bfloat16, device=X.device)
+        Y = _empty((M, w.N), X.device, stream)
     st = w.c_struct()
     _check("qlora_linear_fwd_noalloc", lib().qlora_linear_fwd_noalloc(
         _ptr(_bits(X)), M, ctypes.byref(st), _ptr(_bits(A)), _ptr(_bits(B)), A.shape[0], float(scaling),

@@ -36,14 +36,36 @@ def _calls():
         o = ops.act8_quantize(X, **k)
         return [o.codes, o.scales]
 
-    return {"token_logprob": (lambda **k: [ops.token_logprob(l, y, **k)], 0),
+    X1, wt = X[:16], inputs.weight(3, 0, N, K, 0.05).cuda()
+    bf, dropped = ops.qlora_workspace_bytes, ops.qlora_dropout_workspace_bytes
+
+    def weight(f):
+        def call(**k):
+            o = f(**k)
+            return [o.packed, o.codes, o.scale, o.mean]
+        return call, 0
+
+    older = {"nf4_quantize_dq": weight(lambda **k: ops.nf4_quantize_dq(wt, **k)),
+             "quant4_quantize_dq": weight(lambda **k: ops.quant4_quantize_dq(wt, ops.QLORA_QUANT_FP4, **k)),
+             "nf4_dequant": (lambda **k: [ops.nf4_dequant(W, **k)], 0),
+             "nf4_dequant_merge": (lambda **k: [ops.nf4_dequant_merge(W, A, B, 2.0, **k)], 0),
+             "qlora_linear_fwd": (lambda **k: [ops.qlora_linear_fwd(X, W, A, B, 2.0, **k)], bf(M, N, K, R)),
+             "qlora_linear_fwd of 16": (lambda **k: [ops.qlora_linear_fwd(X1, W, A, B, 2.0, **k)], bf(16, N, K, R)),
+             "qlora_linear_bwd": (lambda **k: list(ops.qlora_linear_bwd(X, dY, W, A, B, 2.0, **k)), bf(M, N, K, R)),
+             "qlora_linear_fwd_dropout": (lambda **k: [ops.qlora_linear_fwd_dropout(X, W, A, B, 2.0, 0.1, 1, 0, **k)],
+                                          dropped(M, N, K, R)),
+             "qlora_linear_bwd_dropout": (lambda **k: list(ops.qlora_linear_bwd_dropout(X, dY, W, A, B, 2.0, 0.1, 1, 0,
+                                                                                        **k)), dropped(M, N, K, R))}
+    return {**older, "token_logprob": (lambda **k: [ops.token_logprob(l, y, **k)], 0),
             "preference_loss": (pref, lw), "policy_loss": (policy, lw),
             "act8_quantize": (quantize, 0), "act8_dequant": (lambda **k: [ops.act8_dequant(x8, **k)], 0),
             "qlora_linear_bwd_act8": (lambda **k: list(ops.qlora_linear_bwd_act8(x8, dY, W, A, B, 2.0, **k)),
                                       ops.qlora_act8_workspace_bytes(M, N, K, R))}
 
 
-NAMES = ["token_logprob", "preference_loss", "policy_loss", "act8_quantize", "act8_dequant", "qlora_linear_bwd_act8"]
+NAMES = ["token_logprob", "preference_loss", "policy_loss", "act8_quantize", "act8_dequant", "qlora_linear_bwd_act8",
+         "nf4_quantize_dq", "quant4_quantize_dq", "nf4_dequant", "nf4_dequant_merge", "qlora_linear_fwd",
+         "qlora_linear_fwd of 16", "qlora_linear_bwd", "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout"]
 
 
 def _blocks(outs, ws):
