@@ -997,10 +997,10 @@ __global__ void __launch_bounds__(NT) k_preference(const PairArgs a) {
         const uint32_t bits = __ballot_sync(0xffffffffu, lng);
         if (lane == 0) sh.is_long[warp] = bits;
         __syncthreads();
-        for (int j = 0; j < NT / 32; ++j) {
-            const int64_t p = (base + 32 * j + warp) * kPairCtas + rank;
+        for (int i = warp; i < NT; i += NT / 32) {
+            const int64_t p = (base + i) * kPairCtas + rank;
             if (p >= a.P) break;
-            if (!((sh.is_long[j] >> warp) & 1u)) acc += do_pair<false, NT>(a, p, sh);
+            if (!((sh.is_long[i >> 5] >> (i & 31)) & 1u)) acc += do_pair<false, NT>(a, p, sh);
         }
         for (int j = 0; j < NT / 32; ++j)
             for (uint32_t b = sh.is_long[j]; b; b &= b - 1) {

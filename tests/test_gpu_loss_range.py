@@ -169,3 +169,19 @@ def test_preference_target_of_probability_zero(eps, M):
     assert o.rewards[worse] == -float("inf") and torch.isfinite(o.rewards[1 - worse])
     assert abs(2 * o.loss.item() - base.loss.item()) <= 1e-6
     assert (o.dlogits[:2] == 0).all() and torch.isfinite(o.dlogits).all()
+
+
+@pytest.mark.parametrize("M,P", [(700, 20), (700, 32), (700, 33), (520, 300), (4000, 2100)])
+def test_every_pair_is_taken(M, P):
+    """Short pairs of every number that the blocks of either width share out: each one's rewards and gradient."""
+    g = np.random.default_rng(P)
+    l = torch.from_numpy(g.standard_normal((M, 40)).astype(np.float32)).cuda()
+    yn = g.integers(0, 40, M)
+    cu = np.sort(g.integers(0, M + 1, 2 * P + 1)).astype(np.int32)
+    o = ops.preference_loss(l, torch.from_numpy(yn).cuda(), torch.from_numpy(cu).cuda(), None, 0.1)
+    loss, rewards, lp, dl, d = tr.preference_loss(l.double().cpu().numpy(), yn, cu, None, 0.1, 0)
+    n = np.diff(cu)
+    # beta = 0.1 times a log-probability's 1e-5 a row; the derivative moves by beta times as much
+    assert (np.abs(o.rewards.cpu().numpy() - rewards) <= 1e-6 * n + 2 * U * np.abs(rewards)).all()
+    e = 0.1 * 1e-6 * (n[0::2] + n[1::2]).max() / P
+    assert (np.abs(o.dlogits.cpu().numpy() - dl) <= 5e-5 * np.abs(d)[:, None] + e).all()
