@@ -98,6 +98,7 @@ def lib():
             "qlora_device_status": (i32, [i32]),
             "qlora_last_path": (i32, []),
             "qlora_pair_schedule": (i32, [i64, i64, i32, i32, P, P, P]),
+            "qlora_pair_schedule_steps": (i32, [i64, i64, i64, i32, i32, P, P, P]),
             "qlora_pair_spans": (i32, [i64, i32, i32, i32, P, i32]),
             "qlora_launch_count": (ctypes.c_longlong, []),
             "qlora_set_kernel_events": (i32, [P, P]),
@@ -583,11 +584,12 @@ def qlora_linear_fwd_noalloc(X, w: NF4Weight, A, B, scaling: float, Y=None, T_ou
     return Y
 
 
-def pair_schedule(M: int, n_out: int, pairs: int, bwd: bool):
-    """(token tiles per weight stage, tile count, stream-K) of the SM-pair kernel."""
+def pair_schedule(M: int, n_out: int, pairs: int, bwd: bool, nsteps: int = 0):
+    """(token tiles per weight stage, tile count, stream-K) of the SM-pair kernel; nsteps: reduction steps of 64, 0 for
+    as many as give every pair a unit."""
     mt, nt, sk = ctypes.c_int(0), ctypes.c_int64(0), ctypes.c_int(0)
-    _check("qlora_pair_schedule", lib().qlora_pair_schedule(M, n_out, pairs, int(bwd), ctypes.byref(mt),
-                                                            ctypes.byref(nt), ctypes.byref(sk)))
+    _check("qlora_pair_schedule_steps", lib().qlora_pair_schedule_steps(
+        M, n_out, nsteps, pairs, int(bwd), ctypes.byref(mt), ctypes.byref(nt), ctypes.byref(sk)))
     return mt.value, nt.value, bool(sk.value)
 
 

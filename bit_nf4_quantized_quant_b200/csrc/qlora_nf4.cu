@@ -292,13 +292,17 @@ constexpr int kSkMaxRp = 64;
 // than running dB and dA after the fused kernel instead of beside it (70B
 // projections at 512 tokens on one box: 1040 -> 1091 TFLOP/s with the forward
 // promoted, 1091 -> 1180 with the backward too).
+// Every pair needs a unit of its own: the owner of a tile waits for a count from each
+// pair between the tile's first one and itself, and a pair with an empty run counts
+// nothing.  With fewer units than pairs (reductions of one or two steps, few tiles)
+// tiles stay whole; the split would gain nothing.  nsteps 0: more than that many.
 struct Tc2Sched {
     int mt;
     bool sk;
     int64_t ntiles;
 };
 
-Tc2Sched tc2_schedule(int64_t M, int64_t n_out, int pairs, bool bwd) {
+Tc2Sched tc2_schedule(int64_t M, int64_t n_out, int64_t nsteps, int pairs, bool bwd) {
     Tc2Sched sc{};
     sc.mt = tc2_token_tiles(M, n_out, pairs);
     const int64_t nt = cdiv(n_out, tc2::BN);
@@ -307,7 +311,8 @@ Tc2Sched tc2_schedule(int64_t M, int64_t n_out, int pairs, bool bwd) {
     if (promote) sc.mt = 2;
     sc.ntiles = cdiv(M, (int64_t)tc2::BM * sc.mt) * nt;
     sc.sk = pairs > 0 && pairs <= kSkMaxPairs && sc.ntiles % pairs != 0 && 3 * sc.ntiles >= pairs &&
-            (promote || sc.ntiles > pairs || 4 * sc.ntiles < 3 * (int64_t)pairs);
+            (promote || sc.ntiles > pairs || 4 * sc.ntiles < 3 * (int64_t)pairs) &&
+            (nsteps == 0 || sc.ntiles * nsteps >= pairs);
     return sc;
 }
 
@@ -396,7 +401,8 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int r, int sms) {
     p.off_Bp = take(big * N * p.rp * 2);
     p.sk_part_bytes = p.sk_flag_bytes = 0;
     if (M > 128) {                      // the SM-pair kernel's path (kPairMinM)
-        for (const Tc2Sched& sc : {tc2_schedule(M, N, kSkMaxPairs, false), tc2_schedule(M, K, kSkMaxPairs, true)}) {
+        for (const Tc2Sched& sc :
+             {tc2_schedule(M, N, 0, kSkMaxPairs, false), tc2_schedule(M, K, 0, kSkMaxPairs, true)}) {
             if (sk_part_bytes(sc, kSkMaxPairs) > p.sk_part_bytes) p.sk_part_bytes = sk_part_bytes(sc, kSkMaxPairs);
             if (sk_flag_bytes(sc) > p.sk_flag_bytes) p.sk_flag_bytes = sk_flag_bytes(sc);
         }
@@ -596,11 +602,7 @@ int launch_tc2(const nf4dq_weight* w, const uint16_t* act, int64_t M, const uint
     a.codes = w->codes; a.scale = w->scale; a.mean = w->mean;
     a.lora_w = lora_w; a.ldl = ldl; a.r = r; a.lper = (int)rup(r, 16); a.nlora = lora ? (int)cdiv(lw, 64) : 0;
     a.out = out; a.M = M; a.N = N; a.K = K; a.n_out = n_out; a.n_red = n_red;
-    Tc2Sched sc = tc2_schedule(M, n_out, pairs, BWD);
-    // every pair needs a unit of its own: the owner of a tile waits for a count from each pair
-    // between the tile's first one and itself, and a pair with an empty run counts nothing
-    // (reductions of one or two steps, few tiles: whole tiles then, the split gains nothing)
-    if (sc.ntiles * (cdiv(n_red, tc2::BK) + a.nlora) < pairs) sc.sk = false;
+    Tc2Sched sc = tc2_schedule(M, n_out, cdiv(n_red, tc2::BK) + a.nlora, pairs, BWD);
     // the counters were zeroed by the kernel before this one (the T or U product), or below
     if (sc.sk && (sk_part_bytes(sc, pairs) > p.sk_part_bytes || sk_flag_bytes(sc) > p.sk_flag_bytes)) sc.sk = false;
     a.sk = sc.sk ? 1 : 0;
@@ -1813,9 +1815,14 @@ int qlora_device_status(int reset) {
 int qlora_last_path(void) { return t_last_path; }
 
 int qlora_pair_schedule(int64_t M, int64_t n_out, int pairs, int bwd, int* mt, int64_t* ntiles, int* stream_k) {
+    return qlora_pair_schedule_steps(M, n_out, 0, pairs, bwd, mt, ntiles, stream_k);
+}
+
+int qlora_pair_schedule_steps(int64_t M, int64_t n_out, int64_t nsteps, int pairs, int bwd, int* mt, int64_t* ntiles,
+                              int* stream_k) {
     if (!mt || !ntiles || !stream_k) return QLORA_ERR_NULL;
-    if (M <= 0 || n_out <= 0 || pairs <= 0) return QLORA_ERR_VALUE;
-    const Tc2Sched sc = tc2_schedule(M, n_out, pairs, bwd != 0);
+    if (M <= 0 || n_out <= 0 || nsteps < 0 || pairs <= 0) return QLORA_ERR_VALUE;
+    const Tc2Sched sc = tc2_schedule(M, n_out, nsteps, pairs, bwd != 0);
     *mt = sc.mt;
     *ntiles = sc.ntiles;
     *stream_k = sc.sk ? 1 : 0;

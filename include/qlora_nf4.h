@@ -417,13 +417,18 @@ QLORA_API int qlora_last_path(void);
  * (N forward, K backward), `pairs` SM pairs and the direction (bwd != 0),
  * writes the token tiles of 256 per weight stage (*mt), the tile count
  * (*ntiles) and 1 to *stream_k when the (tile, reduction step) units are dealt
- * to the pairs stream-K, else 0.  qlora_pair_spans: the spans that pair `pair`
+ * to the pairs stream-K, else 0, for reductions long enough that every pair
+ * gets a unit; qlora_pair_schedule_steps is told the reduction's steps (of 64,
+ * the LoRA ones among them) and says 0 where they are too few (nsteps 0: long
+ * enough).  qlora_pair_spans: the spans that pair `pair`
  * of `npairs` takes of ntiles x nsteps units under stream-K, in the order it
  * takes them: out[3 i] = tile, out[3 i + 1] = first step, out[3 i + 2] = end
  * step (exclusive); writes at most max_spans and returns the span count.
- * Both return QLORA_ERR_VALUE (or QLORA_ERR_NULL) on a bad argument. */
+ * All return QLORA_ERR_VALUE (or QLORA_ERR_NULL) on a bad argument. */
 QLORA_API int qlora_pair_schedule(int64_t M, int64_t n_out, int pairs, int bwd, int* mt, int64_t* ntiles,
                                   int* stream_k);
+QLORA_API int qlora_pair_schedule_steps(int64_t M, int64_t n_out, int64_t nsteps, int pairs, int bwd, int* mt,
+                                        int64_t* ntiles, int* stream_k);
 QLORA_API int qlora_pair_spans(int64_t ntiles, int nsteps, int pair, int npairs, int64_t* out, int max_spans);
 
 /* Measurement hooks (no counterpart on the pages; used by benchmarks).

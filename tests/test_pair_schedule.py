@@ -139,3 +139,23 @@ def test_short_reductions_need_a_unit_for_every_pair(pairs, nsteps):
                     pf = _owner_first_pair(p, pairs, ntiles, nsteps, t)
                     heads = [q for q in range(p) if any(tt == t for (tt, _, _) in spans[q])]
                     assert heads == list(range(pf, p))
+
+
+@pytest.mark.parametrize("pairs", [74, 73, 70, 64])
+@pytest.mark.parametrize("bwd", [False, True])
+def test_the_schedule_knows_the_reduction(pairs, bwd):
+    """With its reduction's steps given, the schedule says stream-K only where every pair has a unit; everything else
+    in it is that of a long reduction."""
+    met = 0
+    for M in (133, 256, 458, 512, 3114):
+        for n_out in range(64, 12000, 64):
+            long = ops.pair_schedule(M, n_out, pairs, bwd)
+            for nsteps in (1, 2, 3, 9):
+                mt, ntiles, sk = ops.pair_schedule(M, n_out, pairs, bwd, nsteps)
+                assert (mt, ntiles) == long[:2] and sk == (long[2] and ntiles * nsteps >= pairs)
+                met += long[2] and not sk
+    assert met
+    # 133 tokens of a 64-wide reduction with LoRA rank 24: two steps, 26 tiles of 6592 columns, 52 units for 74 pairs
+    assert ops.pair_schedule(133, 6592, 74, bwd)[2] and not ops.pair_schedule(133, 6592, 74, bwd, 2)[2]
+    with pytest.raises(ops.QLoRAError):
+        ops.pair_schedule(133, 6592, 74, bwd, -1)
