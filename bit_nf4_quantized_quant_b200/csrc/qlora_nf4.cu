@@ -168,7 +168,8 @@ int check_device(int* sm_count) {
                                         (const void*)k_lora_down_small<4>, (const void*)gmv::k_nf4_gemv_finish<1>,
                                         (const void*)gmv::k_nf4_gemv_finish<2>, (const void*)gmv::k_nf4_gemv_finish<4>,
                                         (const void*)gmv::k_nf4_gemv_finish<8>,
-                                        (const void*)k_lora_bwd_small, (const void*)k_bwd_small_end};
+                                        (const void*)k_lora_bwd_small, (const void*)k_bwd_small_end<0>,
+                                        (const void*)k_bwd_small_end<1>, (const void*)k_bwd_small_end<2>};
                 for (const void* f : smalls)
                     if (r == cudaSuccess)
                         r = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -1005,11 +1006,13 @@ int small_bwd(const Plan& p, const uint16_t* Xl, const act8_tensor* x8, const ui
     e.slots = ta.slots; e.NT = p.NT; e.nks = ta.nks; e.ctas = ta.ctas; e.units = ta.units;
     e.Upart = b.Upart; e.US = p.US; e.A = A; e.X = Xl;
     if (dp) { e.mask = mask; e.c = dp->c; }
-    if (x8) { e.xc = x8->codes; e.xs = x8->scales; e.xfmt = x8->fmt == QLORA_ACT8_E4M3 ? 2 : 1; }
+    if (x8) { e.xc = x8->codes; e.xs = x8->scales; }
     e.M = p.M; e.K = p.K; e.r = p.r; e.rp = p.rp; e.s = scaling; e.dX = dX; e.dA = dA;
     e.s_da = dp ? (float)((double)scaling * (double)dp->c) : scaling;
-    return launch_pdl(k_bwd_small_end, dim3((unsigned)cdiv(p.K, kLoraThreads), (unsigned)(p.M + p.r)),
-                      dim3(kLoraThreads), 0, st, e);
+    void (*end)(BwdEndArgs) = x8 == nullptr                   ? k_bwd_small_end<0>
+                              : x8->fmt == QLORA_ACT8_E4M3 ? k_bwd_small_end<2>
+                                                           : k_bwd_small_end<1>;
+    return launch_pdl(end, dim3((unsigned)cdiv(p.K, kLoraThreads), (unsigned)(p.M + p.r)), dim3(kLoraThreads), 0, st, e);
 }
 
 // Bytes of the dropped copy of X that the dropout entry points need past the

@@ -291,9 +291,8 @@ struct BwdEndArgs {
     const uint16_t* mask;    // LoRA dropout: keep bits of [M, K] (the LoRA term of dX is masked, keep * c,
                              // and X above is then X * keep); null without dropout
     float c;                 // scale of kept values
-    const uint8_t* xc;       // X as an 8-bit checkpoint (xfmt != 0: 1 int8, 2 E4M3): codes [M, K] and
+    const uint8_t* xc;       // X as an 8-bit checkpoint (XF != 0): codes [M, K] and
     const uint8_t* xs;       // scale bytes [M, K / 32]
-    int xfmt;
 };
 
 // The CTA that owns unit u under k_tcs_gemm's even split of U units over C
@@ -305,8 +304,13 @@ __device__ __forceinline__ uint32_t end_unit_owner(uint32_t u, uint32_t U, uint3
 // grid (ceil(K / 256), M + r): row y < M writes dX[y, :], row M + i writes dA[i, :].
 // Launched programmatically after k_tcs_gemm: it lets the next kernel on the
 // stream launch, then waits for that kernel (and so for the U / dB kernel
-// before it).
-__global__ void __launch_bounds__(kLoraThreads) k_bwd_small_end(BwdEndArgs a) {
+// before it).  XF: X is bf16 (0) or an 8-bit checkpoint (1: int8, 2: E4M3); a
+// template parameter, since the code of all three in one kernel took 40 registers,
+// six CTAs an SM instead of eight (T given, 1 token, 4096 x 4096: bf16 16.2 us
+// against 15.4, int8 16.1 against 15.4; 32 tokens, 8192 x 8192 of rank 64: bf16
+// 87.6 against 82.4).  E4M3 spills in the 32 registers of eight CTAs.
+template <int XF>
+__global__ void __launch_bounds__(kLoraThreads, XF == 2 ? 6 : 8) k_bwd_small_end(BwdEndArgs a) {
     __shared__ float s_q[kLoraThreads];
     __shared__ float s_u[kLoraThreads];
     grid_dep_launch();
@@ -355,13 +359,13 @@ __global__ void __launch_bounds__(kLoraThreads) k_bwd_small_end(BwdEndArgs a) {
     } else {
         const int i = y - (int)a.M;
         float v = 0.f;
-        if (a.xfmt == 0) {
+        if (XF == 0) {
             for (int64_t m = 0; m < a.M; ++m) v = __fmaf_rn(s_u[m], bf16lo_to_f32(a.X[m * a.K + k]), v);
         } else {
             for (int64_t m = 0; m < a.M; ++m) {
                 const int64_t e = m * a.K + k;
                 const uint32_t c = a.xc[e];
-                const float x = a.xfmt == 2 ? adam::e4m3x2_to_f32(c).x : (float)(int8_t)c;
+                const float x = XF == 2 ? adam::e4m3x2_to_f32(c).x : (float)(int8_t)c;
                 // rounded to bf16 like the restored tensor (exact but for the smallest scales)
                 const uint32_t xb = pack_bf16x2(x * act8::scale_of(a.xs[e >> 5]), 0.f);
                 v = __fmaf_rn(s_u[m], bf16lo_to_f32(xb), v);
