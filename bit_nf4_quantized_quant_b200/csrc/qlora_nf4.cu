@@ -988,9 +988,10 @@ int small_bwd(const Plan& p, const uint16_t* Xl, const act8_tensor* x8, const ui
     b.b_vec = (p.r % 8 == 0 && aligned16(B)) ? 1 : 0;
     b.Upart = reinterpret_cast<float*>(wsb + p.off_Upart); b.US = p.US; b.u_ctas = (int)(p.US * cdiv(p.M, kUTok)); b.rows_u = p.rows_u; b.dB = dB;
     // behind the T kernel (a plain launch: everything before it has completed) it starts at once, and
-    // only its dB CTAs wait for T
+    // only its dB CTAs wait for T; and with it the fused kernel, beside which a long T takes longer (32
+    // tokens, 11008 x 4096: 44.3 us so, 46.9 one after the other; 4 tokens, 4096 x 11008: 38.8 and 35.8)
     const dim3 grid((unsigned)(b.u_ctas + cdiv(p.N, kLoraThreads)));
-    if (T32) {
+    if (T32 && p.K <= p.N) {
         rc = launch_pdl(k_lora_bwd_small, grid, dim3(kLoraThreads), 0, st, b);
     } else {
         k_lora_bwd_small<<<grid, kLoraThreads, 0, st>>>(b);
