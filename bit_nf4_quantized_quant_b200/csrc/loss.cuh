@@ -1035,12 +1035,17 @@ __global__ void __launch_bounds__(NT) k_preference(const PairArgs a) {
     }
 }
 
-// Pair losses and gradient of up to kFewRows rows and kFewPairs pairs in one
-// launch.  The first CTA takes the losses and the rewards, a pair a warp; each of the others takes a chunk of a
+// Pair losses and gradient of up to kFewRows rows, kFewPairs pairs and kFewBytes
+// of logits in one launch.  The first CTA takes the losses and the rewards, a pair a warp; each of the others takes a chunk of a
 // row, and adds up the row's pair itself while the chunk is on its way: a few
 // hundred values, for which a kernel of its own before this one costs more
-// (one pair of 61 x 32000: 16.5 us in three launches, 12 us in two).
+// (one pair of 61 x 32000: 16.5 us in three launches, 12 us in two).  With more
+// chunks the sums of all of them outweigh the launch (log-probabilities included;
+// in two launches and in three, us): 16 MB 256 x 32000 bf16 17.4 and 18.7, 64 x
+// 128256 bf16 16.0 and 17.9, 512 x 8000 fp32 14.5 and 14.4; 33 MB 512 x 32000 bf16
+// 30.3 and 27.9, 64 x 128256 fp32 23.1 and 20.0; 512 x 262144 fp32 282 and 253.
 constexpr int kFewRows = 512, kFewPairs = 32;
+constexpr int64_t kFewBytes = 1 << 24;
 
 struct FewArgs {
     PairArgs p;

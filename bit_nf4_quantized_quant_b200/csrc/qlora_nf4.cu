@@ -1728,7 +1728,8 @@ int preference_loss(const void* logits, int dtype, int64_t M, int64_t V, int64_t
     g.logits = logits; g.M = M; g.V = (int)V; g.ld = ld; g.tau = logit_scale;
     split_c(logit_scale, &g.c, &g.c_lo, &g.c_rel);
     g.targets = targets; g.lpd = lpd; g.stats = stats; g.dlogp = dlogp; g.out = dlogits; g.ldo = ldd; g.chunks = (int)chunks;
-    if (dlogits && M <= loss::kFewRows && P <= loss::kFewPairs) {
+    if (dlogits && M <= loss::kFewRows && P <= loss::kFewPairs &&
+        M * V * (int64_t)logit_bytes(dtype) <= loss::kFewBytes) {
         const loss::FewArgs fa{a, g};
         return dtype == QLORA_LOGITS_FP32
                    ? launch_rows<loss::FewArgs>(loss::k_preference_few<float>, M * chunks + 1, 1, loss::kGradThreads, st, fa)

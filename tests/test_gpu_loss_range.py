@@ -185,3 +185,28 @@ def test_every_pair_is_taken(M, P):
     assert (np.abs(o.rewards.cpu().numpy() - rewards) <= 1e-6 * n + 2 * U * np.abs(rewards)).all()
     e = 0.1 * 1e-6 * (n[0::2] + n[1::2]).max() / P
     assert (np.abs(o.dlogits.cpu().numpy() - dl) <= 5e-5 * np.abs(d)[:, None] + e).all()
+
+
+@pytest.mark.parametrize("dtype,M,V,P", [("bf16", 255, 32768, 4), ("bf16", 256, 32768, 4), ("bf16", 257, 32768, 4),
+                                         ("fp32", 32, 131072, 1), ("fp32", 33, 131072, 1)])
+def test_preference_on_both_sides_of_the_few_rows(dtype, M, V, P):
+    """Around the bytes of logits up to which the pair terms are taken by the gradient's CTAs: one call against one
+    call a pair, each of them within that bound."""
+    l = (torch.randn((M, V), device="cuda") * 2).to(DT[dtype])
+    y = torch.arange(M, device="cuda") * 37 % V
+    y[::6] = -100
+    cu = torch.linspace(0, M - 1, 2 * P + 1, device="cuda").int()
+    o = ops.preference_loss(l, y, cu, None, 0.05)
+    losses = []
+    for p in range(P):
+        a, b = int(cu[2 * p]), int(cu[2 * p + 2])
+        s = ops.preference_loss(l[a:b], y[a:b], cu[2 * p:2 * p + 3] - a, None, 0.05)
+        losses.append(s.loss.item())
+        # log-probabilities are off by 1e-5 on either side (sums in another order), a sequence's by that times its rows
+        e = 2e-5 * (b - a)
+        assert torch.allclose(o.rewards[2 * p:2 * p + 2], s.rewards, rtol=1e-6, atol=0.05 * e)
+        d = (o.dlogits[a:b].float() * P - s.dlogits.float()).abs()
+        # g moves by beta^2 / 4 of it; p by 2e-5 of itself; two roundings of the type, one of them of the P-th part
+        assert (d <= (2.5 * HALF[dtype] + 4e-5) * s.dlogits.float().abs() + 0.05 ** 2 / 4 * e).all()
+    assert abs(o.loss.item() - np.mean(losses)) <= 0.05 * 2e-5 * M
+    assert (o.dlogits[M - 1] == 0).all()
