@@ -40,11 +40,20 @@ def stale() -> bool:
     return any(os.path.getmtime(s) > t for s in sources())
 
 
+def _torch_stamp() -> str:
+    """What the binding carries of the torch it was built with, whose C++ interface differs from version to version."""
+    import torch
+    return f"built with torch {torch.__version__};"
+
+
 def _binding_stale() -> bool:
     if not os.path.exists(BINDING):
         return True
     t = os.path.getmtime(BINDING)
-    return any(os.path.getmtime(s) > t for s in (BINDING_SRC, HEADER))
+    if any(os.path.getmtime(s) > t for s in (BINDING_SRC, HEADER)):
+        return True
+    with open(BINDING, "rb") as f:
+        return _torch_stamp().encode() not in f.read()
 
 
 def build_binding(force: bool = False) -> str:
@@ -60,7 +69,8 @@ def build_binding(force: bool = False) -> str:
     tmp = f"{BINDING}.tmp{os.getpid()}"
     subprocess.check_call(
         ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f"-I{sysconfig.get_paths()['include']}",
+         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DQLORA_TORCH_STAMP="{_torch_stamp()}"',
+         f"-I{sysconfig.get_paths()['include']}",
          f"-I{inc}", f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}", f"-I{os.path.join(cuda, 'include')}",
          BINDING_SRC, "-o", tmp, f"-L{HERE}", "-l:libqlora_nf4.so", "-Wl,-rpath,$ORIGIN", f"-L{tlib}", "-lc10",
          "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"])

@@ -369,7 +369,8 @@ PyMethodDef kMethods[] = {FAST("bind", py_bind),
                           FAST("preference_loss", py_preference_loss),
                           FAST("policy_loss", py_policy_loss),
                           {nullptr, nullptr, 0, nullptr}};
-PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_step", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
+// the module's docstring; build.py looks for it in the built file
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_step", QLORA_TORCH_STAMP, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
