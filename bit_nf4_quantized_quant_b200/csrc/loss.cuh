@@ -441,7 +441,7 @@ __device__ __noinline__ MS careful_total(const T* x, int V, int v0, int v1, floa
 template <typename T>
 __device__ __forceinline__ void zero_row(T* o, int V, int v0, int v1, uint32_t rank) {
     const Row<T> sp(o, V);
-    // rank q clears vectors [v0, v1), and the last rank that has any also what is left of them
+    // each rank clears its vectors [v0, v1), and rank 0 the head, the tail and what is left of the vectors
     uint4* ov = reinterpret_cast<uint4*>(o + sp.head);
     const int end = v1 < sp.nv ? v1 : sp.nv;
     for (int i = v0 + threadIdx.x; i < end; i += blockDim.x) ov[i] = make_uint4(0, 0, 0, 0);

@@ -33,8 +33,8 @@
 //    then runs beside the one before it on the SMs that one leaves free, and
 //    one CTA waits for it before exiting, so this grid completes after it.
 //  * dA from an 8-bit checkpoint of X (k_colk8): the codes come through the
-//    ring as they are (64 tokens x 128 columns, a quarter of the bytes of the
-//    bf16 tiles per column) and become bf16 in registers, on the way into the
+//    ring as they are (64 tokens x 128 columns, half the bytes of the bf16
+//    tiles per column) and become bf16 in registers, on the way into the
 //    multiply-adds; see there.
 //  * Every mbarrier wait is bounded (an expired wait raises the CTA's abort
 //    flag and the device status); every thread still takes both cluster
