@@ -210,3 +210,34 @@ def test_preference_on_both_sides_of_the_few_rows(dtype, M, V, P):
         assert (d <= (2.5 * HALF[dtype] + 4e-5) * s.dlogits.float().abs() + 0.05 ** 2 / 4 * e).all()
     assert abs(o.loss.item() - np.mean(losses)) <= 0.05 * 2e-5 * M
     assert (o.dlogits[M - 1] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,V", SHAPES)
+def test_far_rows_in_place(M, V, dtype):
+    """Rows far from 0 among ordinary ones, the gradient over the logits and captured: bit for bit the one elsewhere."""
+    l = torch.randn((M, V), device="cuda")
+    l[::3] = l[::3].mul(1e7).sub(1e9)
+    l[1::3] = -1e9
+    l = l.to(DT[dtype])
+    y = torch.arange(M, device="cuda") * 31 % V
+    w = torch.rand(M, device="cuda") + 0.5
+    cu = torch.tensor([0, M // 2, M], dtype=torch.int32, device="cuda")
+    ws = ops.loss_workspace(M)
+    for f in (lambda t, **k: ops.policy_loss(t, y, -w, w, None, None, ws=ws, **k),
+              lambda t, **k: ops.preference_loss(t, y, cu, None, 0.1, average=True, ws=ws, **k)):
+        want = f(l)
+        t = l.clone()
+        got = f(t, dlogits=t)
+        assert torch.equal(want.dlogits, got.dlogits) and torch.equal(want.logp, got.logp)
+        assert torch.isfinite(want.dlogits).all() and torch.isfinite(want.logp).all()
+        t.zero_()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = f(t, dlogits=t)
+        for _ in range(2):
+            t.copy_(l)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(want.dlogits, t) and torch.equal(want.logp, got.logp)
+    assert ops.qlora_device_status() == 0
