@@ -772,7 +772,7 @@ __device__ __forceinline__ void grad_chunk(const GradArgs& a, int64_t row, int c
             v[u] = i0 + u * NT < sp.nv ? ld_v4(xv + i0 + u * NT) : make_uint4(0, 0, 0, 0);
     }
     const float g = y >= 0 ? coef() * a.tau : 0.f;
-    const float q = careful ? g / st.y : grad_factor<T>(g, KS{st.x, st.y}, a.c_rel);
+    const float q = grad_factor<T>(g, careful ? KS{0.f, -st.y} : KS{st.x, st.y}, a.c_rel);
     auto one = [&](float l) { return q * ex2(careful ? (l - st.x) * a.c : grad_exp<T>(l, a.c, a.c_lo, st.x)); };
     auto at_y = [&] { return -g * expm1f((float)a.lpd[row]); };
     auto put = [&](int e) {
@@ -1192,8 +1192,17 @@ __device__ __forceinline__ float policy_row(const PolicyArgs& a, int row, Lp2 lp
 // x 72000 bf16: 652 us, this one 399; 16777 x 32000: 398 and 375).  1 GB of
 // logits: bf16 5.7 TB/s of reads and writes at 32000 (its exponentials, two an
 // element, share the time with the memory), fp32 6.6 TB/s, the rate of a copy.
+// Left to itself the compiler takes a few registers too many for one block more
+// at two widths (600 MB of fp32 logits: 6000 columns 199 us with five blocks an SM,
+// 189 with six; 12280 columns 196 with three, 189 with four; bf16, where it takes
+// fewer, loses 2 % by being told).
 template <typename T, int NV>
-__global__ void __launch_bounds__(kBlockThreads) k_policy_block(const PolicyArgs a) {
+constexpr int policy_ctas() {
+    return sizeof(T) != 4 ? 0 : NV == 12 ? 6 : NV == 24 ? 4 : 0;      // 0: as the compiler likes
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(kBlockThreads, policy_ctas<T, NV>()) k_policy_block(const PolicyArgs a) {
     constexpr int NT = kBlockThreads;
     __shared__ BlockShared sh;
     const uint32_t rank = cluster_rank(), z = cluster_size();
@@ -1276,9 +1285,10 @@ __global__ void __launch_bounds__(kBlockThreads) k_policy_block(const PolicyArgs
     }
 }
 
-// The same for short rows, a warp each.
+// The same for short rows, a warp each; with 16 vectors a lane five blocks an SM
+// instead of four (75000 x 4000 bf16: 243 -> 225 us, 75000 x 2000 fp32 205 -> 201).
 template <typename T, int NT, int NV>
-__global__ void __launch_bounds__(kBlockThreads) k_policy_short(const PolicyArgs a) {
+__global__ void __launch_bounds__(kBlockThreads, NV == 16 ? 5 : 0) k_policy_short(const PolicyArgs a) {
     __shared__ ShortShared sh;
     grid_dep_wait();
     grid_dep_launch();
@@ -1314,7 +1324,7 @@ __global__ void __launch_bounds__(kBlockThreads) k_policy_short(const PolicyArgs
     const float g = policy_row(a, (int)row, lp, A, w, old, ref, id == 0);
     if (a.out == nullptr) return;
     const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
-    const float k = t.k, q = careful ? -g / ms.s : grad_factor<T>(g, t, a.c_rel);
+    const float k = t.k, q = grad_factor<T>(g, careful ? KS{0.f, ms.s} : t, a.c_rel);
     if (g == 0.f) {
         zero_short_row<T, NT>(o, V);
     } else if (careful || !same) {
