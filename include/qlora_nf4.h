@@ -388,6 +388,8 @@ QLORA_API int preference_loss(const void* logits, int dtype, int64_t M, int64_t 
  *   loss = sum of weights (pol + kl_coef kl); with kl_coef = 0 kl is summed for
  *          stats alone
  *   stats [4] = loss, sum w pol, sum w kl, sum of w over the clipped rows
+ * The terms of a row are fp32: rho and exp(d) are infinite where their exponent
+ * is above 88.7, and with an advantage of 0 rho A is 0 all the same.
  * The gradient of pol is zero where the clipped term is the strictly smaller
  * one and -rho A elsewhere.  The weights carry the mask and the normalisation
  * (1 / number of tokens, 1 / (sequences * length), ...).
