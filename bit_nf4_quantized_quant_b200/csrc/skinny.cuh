@@ -566,6 +566,10 @@ __global__ void __launch_bounds__(kThreads) k_colk8(const __grid_constant__ CUte
                     }
                 }
             }
+            // the fence orders the loads above before the copy that refills the stage: released without
+            // it, a stage was overwritten under loads still in flight (3092 x 72 x 28480, 223 CTAs of
+            // 49 stages: dA of 1 call in 19 was off in some columns)
+            tc::fence_proxy_async();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(empty(st));
         }

@@ -209,3 +209,24 @@ def test_refusals_on_the_gpu():
     assert e.value.code == -5
     with pytest.raises(ValueError, match="out"):
         ops.act8_dequant(x8, out=torch.empty((4, 32), dtype=torch.bfloat16, device="cuda"))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K,r", [(3092, 72, 28480, 8), (3092, 1000, 28480, 16), (509, 64, 28672, 16),
+                                     (2000, 128, 12800, 24), (4096, 64, 8192, 64), (2048, 4096, 4096, 16)])
+def test_bwd_repeats_bit_identically(M, N, K, r, fmt):
+    """Hundreds of calls, in long reductions by several CTAs an SM among others: the gradients of the restored tensor
+    bit for bit, every time (a stage of the ring refilled under loads still in flight shows as a rare difference)."""
+    w, X, A, B, dY = _layer(M, N, K, r, M + r)
+    x8 = ops.act8_quantize(X, fmt)
+    T = torch.empty((M, r), dtype=torch.bfloat16, device="cuda")
+    ops.qlora_linear_fwd(X, w, A, B, 2.0, T_out=T)
+    want = ops.qlora_linear_bwd(ops.act8_dequant(x8), dY, w, A, B, 2.0, T=T)
+    ws = ops.act8_workspace(M, N, K, r)
+    off = torch.zeros(3, dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        got = ops.qlora_linear_bwd_act8(x8, dY, w, A, B, 2.0, T=T, ws=ws)
+        for i in range(3):
+            off[i] += (got[i].view(torch.int16) != want[i].view(torch.int16)).any()
+    assert off.tolist() == [0, 0, 0]
+    assert ops.qlora_device_status() == 0
