@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_nf4_gemv(const __grid_constant_
                     mma_bf16_16816(acc[nt], oa[2], ob[2], oa[3], ob[3], x2, x3);
                 }
             }
+            tc::fence_proxy_async();              // the loads above before the copy that refills the stage
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(empty(st));
         };

@@ -228,6 +228,9 @@ __device__ __forceinline__ void run(const CUtensorMap* tmP, const CUtensorMap* t
 #pragma unroll
                 for (int t = 0; t < JQ / 8; ++t) mma_bf16_16816(acc[t], a0, a1, a2, a3, b[t][0], b[t][1]);
             }
+            // the loads above before the copy that refills the stage (0.4 % of the 7B block's step, 0.8 %
+            // of the 70B one at 512 tokens; see k_colk8)
+            tc::fence_proxy_async();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(empty(st));
         }
@@ -568,7 +571,8 @@ __global__ void __launch_bounds__(kThreads) k_colk8(const __grid_constant__ CUte
             }
             // the fence orders the loads above before the copy that refills the stage: released without
             // it, a stage was overwritten under loads still in flight (3092 x 72 x 28480, 223 CTAs of
-            // 49 stages: dA of 1 call in 19 was off in some columns)
+            // 49 stages: dA of 1 call in 19 was off in some columns; dB by way of a T recomputed on 392
+            // CTAs of 56 stages, of 1 call in 6000)
             tc::fence_proxy_async();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(empty(st));

@@ -230,3 +230,18 @@ def test_bwd_repeats_bit_identically(M, N, K, r, fmt):
             off[i] += (got[i].view(torch.int16) != want[i].view(torch.int16)).any()
     assert off.tolist() == [0, 0, 0]
     assert ops.qlora_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_bwd_with_t_recomputed_repeats_bit_identically(fmt):
+    """The same for the T product, whose ring is the longest here (56 stages on 392 CTAs, three an SM)."""
+    M, N, K, r = 3092, 72, 28480, 8
+    w, X, A, B, dY = _layer(M, N, K, r, 5)
+    x8 = ops.act8_quantize(X, fmt)
+    ws = ops.act8_workspace(M, N, K, r)
+    want = ops.qlora_linear_bwd(ops.act8_dequant(x8), dY, w, A, B, 2.0)
+    off = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(3000):
+        got = ops.qlora_linear_bwd_act8(x8, dY, w, A, B, 2.0, ws=ws)
+        off += sum((g.view(torch.int16) != t.view(torch.int16)).any() for g, t in zip(got, want))
+    assert off.item() == 0 and ops.qlora_device_status() == 0
