@@ -53,7 +53,7 @@ _GEMV_SRC = ("common.cuh", "nf4_decode.cuh", "tc_gemm.cuh", "gemv_mma.cuh", "sma
 TRAFFIC = {
     "workload3_M2048": {"bytes_per_launch": 53644014, "files": _PAIR_SRC, "src": "bcf023ea0d53"},
     # small M: one forward chain (GEMV + T + finish) per projection
-    "workload2_M1": {"bytes_per_launch": 24058496, "files": _GEMV_SRC, "src": "4652662f57b4"},
+    "workload2_M1": {"bytes_per_launch": 24066816, "files": _GEMV_SRC, "src": "61bd1fbebd4a"},
 }
 
 
